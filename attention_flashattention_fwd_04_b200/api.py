@@ -66,6 +66,17 @@ SIGNATURES = {
                              _c_i, _c_i, _c_i, _c_f, _c_p]),
     "paged_prefill_append": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i,
                                     _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_f, _c_p]),
+    "attn_rope": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_p, _c_p, _c_i,
+                         _c_p]),
+    "paged_kv_append_fp8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
+                                   _c_i, _c_p]),
+    "paged_rope_append_fp8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i,
+                                     _c_i, _c_i, _c_i, _c_i, _c_i, _c_i, _c_p]),
+    "paged_kv_gather_fp8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
+                                   _c_i, _c_p]),
+    "paged_attn_decode_fp8_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_i]),
+    "paged_attn_decode_fp8": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_p, _c_p, _c_i, _c_i, _c_i, _c_i, _c_i,
+                                     _c_i, _c_f, _c_p, _c_sz, _c_p]),
 }
 
 # Size of the scratch array built into the library for paged_attn_decode_noalloc.
@@ -601,4 +612,326 @@ def attn_fwd_bias(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bias: torch
                              d, int(bool(causal)), float(scale), bias.data_ptr(), strides[0], strides[1], strides[2],
                              _stream_handle(stream))
     _check(rc, "attn_fwd_bias")
+    return out, lse
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions with several axes
+# ----------------------------------------------------------------------------
+
+class RopeSpec(ctypes.Structure):
+    """A rotation: which frequencies turn by which position (attn_rope_spec).
+    Made by :func:`rope_spec`; plain host memory, reusable for every call."""
+
+    _fields_ = [("rot_dim", ctypes.c_int), ("num_axes", ctypes.c_int), ("adjacent_pairs", ctypes.c_int),
+                ("reserved", ctypes.c_int), ("inv_freq", ctypes.c_double * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+def rope_spec(d: int, sections=None, theta: float = 10000.0, rot_dim: int | None = None, adjacent_pairs: bool = False,
+              interleaved_sections: bool = False, inv_freq=None) -> RopeSpec:
+    """The rotation of the first ``rot_dim`` (default d) values of each head.
+
+    ``sections``: how many of the rot_dim / 2 frequencies each axis has, in the
+    order of the positions' axes (default: one axis).  They follow one another,
+    or, with ``interleaved_sections``, take turns while they last (t h w t h w
+    ...).  ``inv_freq``: the rot_dim / 2 frequencies in radians a position
+    (default theta ** (-2 j / rot_dim)), e.g. rescaled ones for long contexts.
+    ``adjacent_pairs``: pairs (2j, 2j + 1) instead of (j, j + rot_dim / 2).
+    """
+    rot = d if rot_dim is None else int(rot_dim)
+    if d not in (64, 128) or rot < 16 or rot > d or rot % 16:
+        raise ValueError(f"rot_dim must be a multiple of 16 up to d (64 or 128), got {rot} of {d}")
+    half = rot // 2
+    sections = [half] if sections is None else [int(n) for n in sections]
+    if not sections or len(sections) > 255 or min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections {sections} do not share out {half} frequencies")
+    if interleaved_sections:
+        left, order = list(sections), []
+        while len(order) < half:
+            for a in range(len(left)):
+                if left[a]:
+                    left[a] -= 1
+                    order.append(a)
+    else:
+        order = [a for a, n in enumerate(sections) for _ in range(n)]
+    freq = [float(theta) ** (-2.0 * j / rot) for j in range(half)] if inv_freq is None else [float(f) for f in inv_freq]
+    if len(freq) != half:
+        raise ValueError(f"inv_freq has {len(freq)} entries, not {half}")
+    spec = RopeSpec(rot, len(sections), int(bool(adjacent_pairs)), 0)
+    spec.inv_freq[:half] = freq
+    spec.axis[:half] = order
+    return spec
+
+
+def _one_device(**tensors):
+    """Checks, after the shapes, that the tensors (None left out) are on one
+    CUDA device; returns it."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return device
+
+
+def _launch_stream(stream, device):
+    """The stream of a call: the current one of ``device``, or the given one, which must be a stream of it."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream
+
+
+def _rope_tensor(x, name, out, out_name):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != torch.bfloat16 or x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a 3-d or 4-d bfloat16 tensor, got {x.dtype} {tuple(x.shape)}")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != x.shape):
+        raise ValueError(f"{out_name} must be a bfloat16 tensor of {name}'s shape")
+    for t, what in ((x, name), (out, out_name)):
+        if t is not None and t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"the rows of {what} must be contiguous")
+
+
+def _rope_strides(x):
+    """{batch, head, token} strides of [B, H, N, d] or packed [T, H, d]."""
+    s = x.stride()
+    return (ctypes.c_longlong * 3)(s[0], s[1], s[2]) if x.dim() == 4 else (ctypes.c_longlong * 3)(0, s[1], s[0])
+
+
+def attn_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, spec: RopeSpec, inverse: bool = False,
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Rotary positions with several axes on queries and keys.
+
+    q [B,Hq,N,d] and k [B,Hkv,N,d] bf16 with positions [axes,B,N] int32, or
+    packed q [T,Hq,d], k [T,Hkv,d] with positions [axes,T]; ``k`` may be None.
+    Rows must be contiguous, the other strides are free (multiples of 8).
+    ``inverse`` turns back, which is the gradient.  ``q_out`` / ``k_out`` may be
+    q / k.  Returns (q_out, k_out), bf16."""
+    _rope_tensor(q, "q", q_out, "q_out")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    else:
+        _rope_tensor(k, "k", k_out, "k_out")
+    if q.dim() == 4:
+        B, Hq, N, d = q.shape
+        where = (B, N)
+    else:
+        N, Hq, d = q.shape
+        B, where = 1, (N,)
+    if k is not None:
+        Hkv = k.shape[1]
+        if k.shape != ((B, Hkv, N, d) if q.dim() == 4 else (N, Hkv, d)):
+            raise ValueError(f"k shape {tuple(k.shape)} does not match q {tuple(q.shape)}")
+    if not isinstance(spec, RopeSpec):
+        raise TypeError("spec must come from rope_spec")
+    _require(positions, "positions", torch.int32, 1 + len(where), cuda=False)
+    if positions.shape != (spec.num_axes, *where):
+        raise ValueError(f"positions must be {(spec.num_axes, *where)}, got {tuple(positions.shape)}")
+    device = _one_device(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
+    s = _launch_stream(stream, device)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        has_k = k is not None
+        rc = lib().attn_rope(q.data_ptr(), q_out.data_ptr(), _rope_strides(q), _rope_strides(q_out), Hq,
+                             k.data_ptr() if has_k else None, k_out.data_ptr() if has_k else None,
+                             _rope_strides(k) if has_k else None, _rope_strides(k_out) if has_k else None,
+                             Hkv if has_k else 0, B, N, d, positions.data_ptr(), ctypes.byref(spec), int(bool(inverse)),
+                             s.cuda_stream)
+    _check(rc, "attn_rope")
+    return q_out, k_out
+
+
+# ----------------------------------------------------------------------------
+# The paged KV cache in 8 bits
+# ----------------------------------------------------------------------------
+
+def kv_cache_fp8(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda"):
+    """An empty 8-bit cache: (k_pool, v_pool, kv_scales), zeroed, in the types and layouts the calls below take."""
+    pools = [torch.zeros((num_pages, page_size, Hkv, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+    scales = torch.full((num_pages, Hkv, page_size, 2), 127, dtype=torch.uint8, device=device)
+    return pools[0], pools[1], scales.view(torch.float8_e8m0fnu)
+
+
+def _cache8_args(k_pool, v_pool, kv_scales, block_table, seq_lens, others):
+    """Types and shapes shared by the calls on the 8-bit cache, before any CUDA call.
+    ``others``: (tensor or None, name, dtype, dims) of the rest.  Returns
+    (S, num_pages, page_size, Hkv, d, max_pages)."""
+    for t, name, kind in ((k_pool, "k_pool", torch.float8_e4m3fn), (v_pool, "v_pool", torch.float8_e4m3fn),
+                          (kv_scales, "kv_scales", torch.float8_e8m0fnu)):
+        _require(t, name, torch.uint8 if isinstance(t, torch.Tensor) and t.dtype == torch.uint8 else kind, 4, cuda=False)
+    _require(block_table, "block_table", torch.int32, 2, cuda=False)
+    _require(seq_lens, "seq_lens", torch.int32, 1, cuda=False)
+    num_pages, page_size, Hkv, d = k_pool.shape
+    if v_pool.shape != k_pool.shape:
+        raise ValueError(f"v_pool shape {tuple(v_pool.shape)} differs from k_pool's {tuple(k_pool.shape)}")
+    if kv_scales.shape != (num_pages, Hkv, page_size, 2):
+        raise ValueError(f"kv_scales must be {(num_pages, Hkv, page_size, 2)}, got {tuple(kv_scales.shape)}")
+    S = seq_lens.shape[0]
+    if block_table.shape[0] != S:
+        raise ValueError(f"block_table {tuple(block_table.shape)} does not have one row per sequence ({S})")
+    for t, name, kind, nd in others:
+        if t is not None:
+            _require(t, name, kind, nd, cuda=False)
+    return S, num_pages, page_size, Hkv, d, block_table.shape[1]
+
+
+def _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d):
+    if k_new.shape[1:] != (Hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new {tuple(k_new.shape)} / v_new {tuple(v_new.shape)} do not match the pools")
+    if cu_seqlens_q.shape[0] != seq_lens.shape[0] + 1:
+        raise ValueError("cu_seqlens_q does not match the number of sequences")
+
+
+def paged_kv_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                        kv_scales: torch.Tensor, block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                        seq_lens: torch.Tensor, stream=None):
+    """paged_kv_append into an 8-bit cache: quantises the new rows (packed
+    [total_q,Hkv,d] bf16) as they are written.  k_pool / v_pool
+    [num_pages,page_size,Hkv,d] float8_e4m3fn and kv_scales
+    [num_pages,Hkv,page_size,2] float8_e8m0fnu (uint8 views of them are taken
+    too), see kv_cache_fp8.  In place."""
+    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
+        k_pool, v_pool, kv_scales, block_table, seq_lens,
+        [(k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
+         (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)])
+    _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
+    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens,
+                         k_new=k_new, v_new=v_new, cu_seqlens_q=cu_seqlens_q)
+    s = _launch_stream(stream, device)
+    with torch.cuda.device(device):
+        rc = lib().paged_kv_append_fp8(k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                                       kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                                       block_table.data_ptr(), S, k_new.shape[0], Hkv, d, page_size, max_pages, num_pages,
+                                       s.cuda_stream)
+    _check(rc, "paged_kv_append_fp8")
+
+
+def paged_rope_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
+                          spec: RopeSpec, k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor,
+                          block_table: torch.Tensor, cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor,
+                          q_out: torch.Tensor | None = None, stream=None):
+    """attn_rope on a step's q [total_q,Hq,d] and k_new and
+    paged_kv_append_fp8, in one kernel (positions [axes,total_q] int32).  The
+    cache is updated in place; ``q_out`` may be q.  Returns q_out; its rows
+    behind cu_seqlens_q[-1] are not written."""
+    if not isinstance(spec, RopeSpec):
+        raise TypeError("spec must come from rope_spec")
+    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
+        k_pool, v_pool, kv_scales, block_table, seq_lens,
+        [(q, "q", torch.bfloat16, 3), (k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
+         (q_out, "q_out", torch.bfloat16, 3), (positions, "positions", torch.int32, 2),
+         (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)])
+    _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
+    total_q, Hq = q.shape[:2]
+    if q.shape != (k_new.shape[0], Hq, d) or (q_out is not None and q_out.shape != q.shape):
+        raise ValueError("q / q_out do not match k_new")
+    if positions.shape != (spec.num_axes, total_q):
+        raise ValueError(f"positions must be {(spec.num_axes, total_q)}, got {tuple(positions.shape)}")
+    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, q=q,
+                         k_new=k_new, v_new=v_new, positions=positions, cu_seqlens_q=cu_seqlens_q, q_out=q_out)
+    s = _launch_stream(stream, device)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        rc = lib().paged_rope_append_fp8(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
+                                         positions.data_ptr(), ctypes.byref(spec), k_pool.data_ptr(), v_pool.data_ptr(),
+                                         kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                                         block_table.data_ptr(), S, total_q, Hq, Hkv, d, page_size, max_pages, num_pages,
+                                         s.cuda_stream)
+    _check(rc, "paged_rope_append_fp8")
+    return q_out
+
+
+def paged_kv_gather_fp8(k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor, block_table: torch.Tensor,
+                        seq_lens: torch.Tensor, cu_seqlens_k: torch.Tensor, total_rows: int | None = None,
+                        k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """Read an 8-bit cache back as bf16 rows (exact): token t of sequence s
+    goes to row cu_seqlens_k[s] + t of k_out / v_out [total_rows,Hkv,d].  Give
+    the outputs, or ``total_rows`` to have them made (rows that no token falls
+    on are then undefined).  Returns (k_out, v_out)."""
+    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
+        k_pool, v_pool, kv_scales, block_table, seq_lens,
+        [(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1), (k_out, "k_out", torch.bfloat16, 3),
+         (v_out, "v_out", torch.bfloat16, 3)])
+    if cu_seqlens_k.shape[0] != S + 1:
+        raise ValueError("cu_seqlens_k does not match the number of sequences")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both k_out and v_out, or neither")
+    if k_out is not None:
+        rows = k_out.shape[0]
+        if k_out.shape != (rows, Hkv, d) or v_out.shape != k_out.shape or total_rows not in (None, rows):
+            raise ValueError(f"k_out / v_out must be [rows, {Hkv}, {d}] alike, got {tuple(k_out.shape)} / "
+                             f"{tuple(v_out.shape)}")
+    elif total_rows is None or total_rows < 0:
+        raise ValueError("total_rows (or k_out and v_out) is needed")
+    else:
+        rows = int(total_rows)
+    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens,
+                         cu_seqlens_k=cu_seqlens_k, k_out=k_out, v_out=v_out)
+    s = _launch_stream(stream, device)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if k_out is None:
+            k_out = torch.empty((rows, Hkv, d), dtype=torch.bfloat16, device=device)
+            v_out = torch.empty_like(k_out)
+        rc = lib().paged_kv_gather_fp8(k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
+                                       seq_lens.data_ptr(), cu_seqlens_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), S,
+                                       rows, Hkv, d, page_size, max_pages, num_pages, s.cuda_stream)
+    _check(rc, "paged_kv_gather_fp8")
+    return k_out, v_out
+
+
+def paged_attn_decode_fp8_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, d: int, max_pages: int, page_size: int) -> int:
+    return int(lib().paged_attn_decode_fp8_workspace_bytes(num_seqs, Hq, Hkv, d, max_pages, page_size))
+
+
+def paged_attn_decode_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor,
+                          block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float | None = None,
+                          workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | None = None, stream=None):
+    """paged_attn_decode over an 8-bit cache (see paged_kv_append_fp8).
+
+    q [S,Hq,d] bf16; block_table [S,max_pages] int32; seq_lens [S] int32, 0
+    giving O = 0 and LSE = -inf.  Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32)."""
+    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
+        k_pool, v_pool, kv_scales, block_table, seq_lens,
+        [(q, "q", torch.bfloat16, 3), (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2)])
+    Hq = q.shape[1]
+    if q.shape != (S, Hq, d):
+        raise ValueError(f"q must be [{S}, Hq, {d}], got {tuple(q.shape)}")
+    if out is not None and out.shape != q.shape:
+        raise ValueError(f"out shape {tuple(out.shape)} differs from q's {tuple(q.shape)}")
+    if lse is not None and lse.shape != (S, Hq):
+        raise ValueError(f"lse shape {tuple(lse.shape)} is not ({S}, {Hq})")
+    if scale is None:
+        scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
+    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, q=q,
+                         out=out, lse=lse, workspace=workspace)
+    s = _launch_stream(stream, device)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if workspace is None:
+            need = paged_attn_decode_fp8_workspace_bytes(S, Hq, Hkv, d, max_pages, page_size)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
+        rc = lib().paged_attn_decode_fp8(
+            q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), page_size, out.data_ptr(), lse.data_ptr(), S, Hq, Hkv, d, max_pages, num_pages,
+            float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s.cuda_stream)
+    _check(rc, "paged_attn_decode_fp8")
     return out, lse

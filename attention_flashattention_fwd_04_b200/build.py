@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libattn_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["attn_api.cu", "attn_noalloc.cu"]
+SOURCES = ["attn_lib.cu", "attn_noalloc.cu"]  # attn_lib.cu includes attn_api.cu
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,286 @@
+// The library's main translation unit: the entry points of attn_api.cu and,
+// on top of its host helpers and its device error word (one word a translation
+// unit), those of the rotary positions and of the 8-bit paged cache.
+#include "attn_api.cu"
+
+#include "cache8.cuh"
+#include "decode8_sm100.cuh"
+#include "rope.cuh"
+
+namespace {
+
+// ----------------------------------------------------------------------------
+// Rotary positions
+// ----------------------------------------------------------------------------
+
+// Checks a rotation and lays its table out for the kernels: frequencies in
+// turns, as fractions of 2^64 (long double holds all 64 bits).
+int rope_table(const attn_rope_spec* spec, int d, attn::RopeTable* out) {
+  if (!spec) return ATTN_ERR_NULL;
+  if (spec->rot_dim < 16 || spec->rot_dim > d || spec->rot_dim % 16 != 0) return ATTN_ERR_SHAPE;
+  if (spec->num_axes < 1 || spec->num_axes > 255) return ATTN_ERR_SHAPE;
+  if (spec->adjacent_pairs != 0 && spec->adjacent_pairs != 1) return ATTN_ERR_SHAPE;
+  *out = attn::RopeTable{};
+  out->half = spec->rot_dim / 2;
+  out->adjacent = spec->adjacent_pairs;
+  for (int j = 0; j < out->half; ++j) {
+    if (!std::isfinite(spec->inv_freq[j]) || spec->axis[j] >= spec->num_axes) return ATTN_ERR_SHAPE;
+    long double turns = static_cast<long double>(spec->inv_freq[j]) / 6.283185307179586476925286766559L;
+    turns = ldexpl(turns - floorl(turns), 64);
+    out->turn[j] = turns >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(turns + 0.5L);
+    out->axis[j] = spec->axis[j];
+  }
+  return ATTN_OK;
+}
+
+// One of the two tensors of attn_rope.  Strides are in elements.
+int rope_tensor(const attn_bf16* x, attn_bf16* out, const long long* strides, const long long* out_strides, int B, int H,
+                int N, attn::RopeTensor* t) {
+  if (!x || !out || !strides || !out_strides) return ATTN_ERR_NULL;
+  if (H < 1) return ATTN_ERR_SHAPE;
+  const int sizes[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0 || out_strides[i] < 0) return ATTN_ERR_SHAPE;
+    if (sizes[i] > 1 && out_strides[i] == 0) return ATTN_ERR_SHAPE;  // rows of the output would fall together
+  }
+  for (int i = 0; i < 3; ++i)  // the stride of a size of 1 is never used
+    if (sizes[i] > 1 && (strides[i] % 8 != 0 || out_strides[i] % 8 != 0)) return ATTN_ERR_ALIGN;
+  if (misaligned16(x) || misaligned16(out)) return ATTN_ERR_ALIGN;
+  t->x = reinterpret_cast<const __nv_bfloat16*>(x);
+  t->out = reinterpret_cast<__nv_bfloat16*>(out);
+  t->b = strides[0];
+  t->h = strides[1];
+  t->n = strides[2];
+  t->ob = out_strides[0];
+  t->oh = out_strides[1];
+  t->on = out_strides[2];
+  t->H = H;
+  return ATTN_OK;
+}
+
+// ----------------------------------------------------------------------------
+// The 8-bit cache
+// ----------------------------------------------------------------------------
+
+// Checks shared by the calls on the 8-bit cache (no CUDA call).
+int validate_cache8(const void* k_pool, const void* v_pool, const void* kv_scales, const int32_t* block_table,
+                    const int32_t* seq_lens, int num_seqs, int Hkv, int d, int page_size, int max_pages, int num_pages) {
+  if (!k_pool || !v_pool || !kv_scales || !block_table || !seq_lens) return ATTN_ERR_NULL;
+  if (num_seqs < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_SHAPE;
+  if (d != 64 && d != 128) return ATTN_ERR_SHAPE;
+  if (num_seqs > 65535 || Hkv > 65535) return ATTN_ERR_SHAPE;
+  if (static_cast<long long>(num_pages) * page_size > INT_MAX || static_cast<long long>(max_pages) * page_size > INT_MAX)
+    return ATTN_ERR_SHAPE;
+  if (page_size % 16 != 0 || page_size > 256) return ATTN_ERR_UNSUPPORTED;
+  if (misaligned16(k_pool) || misaligned16(v_pool) || misaligned16(kv_scales) || misaligned4(block_table) ||
+      misaligned4(seq_lens))
+    return ATTN_ERR_ALIGN;
+  return ATTN_OK;
+}
+
+template <int D, bool ROPE>
+int launch_append8(const attn::RopeTable& table, const attn::Append8Params& p, cudaStream_t stream) {
+  const long long warps = p.total_q;
+  const unsigned grid = static_cast<unsigned>((warps * 32 + attn::kAppend8Threads - 1) / attn::kAppend8Threads);
+  attn::append8_kernel<D, ROPE><<<grid, attn::kAppend8Threads, 0, stream>>>(table, p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
+}
+
+int append8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, attn_bf16* q_out, const int32_t* positions,
+            const attn_rope_spec* spec, bool rope, uint8_t* k_pool, uint8_t* v_pool, uint8_t* kv_scales,
+            const int32_t* cu_seqlens_q, const int32_t* seq_lens, const int32_t* block_table, int num_seqs, int total_q,
+            int Hq, int Hkv, int d, int page_size, int max_pages, int num_pages, void* stream) {
+  const int st = validate_cache8(k_pool, v_pool, kv_scales, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_pages,
+                                 num_pages);
+  if (st != ATTN_OK) return st;
+  if (!cu_seqlens_q) return ATTN_ERR_NULL;
+  if (total_q < 0) return ATTN_ERR_SHAPE;
+  if (misaligned4(cu_seqlens_q)) return ATTN_ERR_ALIGN;
+  attn::RopeTable table{};
+  if (rope) {
+    if (Hq < 1 || Hq > 65535) return ATTN_ERR_SHAPE;
+    const int rs = rope_table(spec, d, &table);
+    if (rs != ATTN_OK) return rs;
+  }
+  if (total_q == 0) return ATTN_OK;
+  if (!k_new || !v_new || (rope && (!q || !q_out || !positions))) return ATTN_ERR_NULL;
+  if (misaligned16(k_new) || misaligned16(v_new)) return ATTN_ERR_ALIGN;
+  if (rope && (misaligned16(q) || misaligned16(q_out) || misaligned4(positions))) return ATTN_ERR_ALIGN;
+  attn::Append8Params p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
+  p.q_out = reinterpret_cast<__nv_bfloat16*>(q_out);
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.kv_scales = kv_scales;
+  p.positions = positions;
+  p.cu_q = cu_seqlens_q;
+  p.seq_lens = seq_lens;
+  p.block_table = block_table;
+  p.num_seqs = num_seqs;
+  p.total_q = total_q;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 128) return rope ? launch_append8<128, true>(table, p, s) : launch_append8<128, false>(table, p, s);
+  return rope ? launch_append8<64, true>(table, p, s) : launch_append8<64, false>(table, p, s);
+}
+
+template <int D>
+int launch_decode8(const attn::Decode8Params& p, attn_bf16* o, float* lse, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.d.max_splits), static_cast<unsigned>(p.d.S), static_cast<unsigned>(p.d.Hq));
+  attn::decode8_split_kernel<D><<<grid, attn::kDecode8Threads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e);
+  const long long warps = static_cast<long long>(p.d.S) * p.d.Hq;
+  const unsigned mgrid = static_cast<unsigned>((warps * 32 + attn::kMergeThreads - 1) / attn::kMergeThreads);
+  attn::decode_merge_kernel<D><<<mgrid, attn::kMergeThreads, 0, stream>>>(p.d, reinterpret_cast<__nv_bfloat16*>(o), lse);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope(const attn_bf16* q, attn_bf16* q_out, const long long* q_strides, const long long* q_out_strides, int Hq,
+              const attn_bf16* k, attn_bf16* k_out, const long long* k_strides, const long long* k_out_strides, int Hkv,
+              int B, int N, int d, const int32_t* positions, const attn_rope_spec* spec, int inverse, void* stream) {
+  if (B < 0 || N < 0) return ATTN_ERR_SHAPE;
+  if (d != 64 && d != 128) return ATTN_ERR_SHAPE;
+  if (inverse != 0 && inverse != 1) return ATTN_ERR_SHAPE;
+  const long long tokens = static_cast<long long>(B) * N;
+  if (tokens > INT_MAX) return ATTN_ERR_SHAPE;
+  attn::RopeTable table;
+  const int st = rope_table(spec, d, &table);
+  if (st != ATTN_OK) return st;
+  if (tokens == 0) return ATTN_OK;
+  if (!positions) return ATTN_ERR_NULL;
+  attn::RopeParams p{};
+  int ts = rope_tensor(q, q_out, q_strides, q_out_strides, B, Hq, N, &p.q);
+  if (ts != ATTN_OK) return ts;
+  if (k || k_out) {
+    ts = rope_tensor(k, k_out, k_strides, k_out_strides, B, Hkv, N, &p.k);
+    if (ts != ATTN_OK) return ts;
+  }
+  if (misaligned4(positions)) return ATTN_ERR_ALIGN;
+  p.positions = positions;
+  p.B = B;
+  p.N = N;
+  p.sign = inverse ? -1.f : 1.f;
+  const unsigned grid = static_cast<unsigned>((tokens * 32 + attn::kRopeThreads - 1) / attn::kRopeThreads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 128)
+    attn::rope_kernel<128><<<grid, attn::kRopeThreads, 0, s>>>(table, p);
+  else
+    attn::rope_kernel<64><<<grid, attn::kRopeThreads, 0, s>>>(table, p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
+}
+
+int paged_kv_append_fp8(const attn_bf16* k_new, const attn_bf16* v_new, uint8_t* k_pool, uint8_t* v_pool, uint8_t* kv_scales,
+                        const int32_t* cu_seqlens_q, const int32_t* seq_lens, const int32_t* block_table, int num_seqs,
+                        int total_q, int Hkv, int d, int page_size, int max_pages, int num_pages, void* stream) {
+  return append8(nullptr, k_new, v_new, nullptr, nullptr, nullptr, false, k_pool, v_pool, kv_scales, cu_seqlens_q, seq_lens,
+                 block_table, num_seqs, total_q, 0, Hkv, d, page_size, max_pages, num_pages, stream);
+}
+
+int paged_rope_append_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, attn_bf16* q_out,
+                          const int32_t* positions, const attn_rope_spec* spec, uint8_t* k_pool, uint8_t* v_pool,
+                          uint8_t* kv_scales, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                          const int32_t* block_table, int num_seqs, int total_q, int Hq, int Hkv, int d, int page_size,
+                          int max_pages, int num_pages, void* stream) {
+  return append8(q, k_new, v_new, q_out, positions, spec, true, k_pool, v_pool, kv_scales, cu_seqlens_q, seq_lens,
+                 block_table, num_seqs, total_q, Hq, Hkv, d, page_size, max_pages, num_pages, stream);
+}
+
+int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* cu_seqlens_k, attn_bf16* k_out, attn_bf16* v_out,
+                        int num_seqs, int total_rows, int Hkv, int d, int page_size, int max_pages, int num_pages,
+                        void* stream) {
+  const int st = validate_cache8(k_pool, v_pool, kv_scales, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_pages,
+                                 num_pages);
+  if (st != ATTN_OK) return st;
+  if (!cu_seqlens_k) return ATTN_ERR_NULL;
+  if (total_rows < 0) return ATTN_ERR_SHAPE;
+  if (misaligned4(cu_seqlens_k)) return ATTN_ERR_ALIGN;
+  if (total_rows == 0) return ATTN_OK;
+  if (!k_out || !v_out) return ATTN_ERR_NULL;
+  if (misaligned16(k_out) || misaligned16(v_out)) return ATTN_ERR_ALIGN;
+  attn::Gather8Params p{};
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.kv_scales = kv_scales;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_k = cu_seqlens_k;
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  p.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  p.num_seqs = num_seqs;
+  p.total_rows = total_rows;
+  p.Hkv = Hkv;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(total_rows) * 32 + attn::kGather8Threads - 1) /
+                                              attn::kGather8Threads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 128)
+    attn::gather8_kernel<128><<<grid, attn::kGather8Threads, 0, s>>>(p);
+  else
+    attn::gather8_kernel<64><<<grid, attn::kGather8Threads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
+}
+
+size_t paged_attn_decode_fp8_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size) {
+  DecodePlan pl;
+  if (Hkv < 1 || !decode_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return 0;
+  return pl.total;
+}
+
+int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales,
+                          const int32_t* block_table, const int32_t* seq_lens, int page_size, attn_bf16* o, float* lse,
+                          int num_seqs, int Hq, int Hkv, int d, int max_pages, int num_pages, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!q || !o || !lse) return ATTN_ERR_NULL;
+  const int st = validate_cache8(k_pool, v_pool, kv_scales, block_table, seq_lens, num_seqs, Hkv, d, page_size, max_pages,
+                                 num_pages);
+  if (st != ATTN_OK && st != ATTN_ERR_UNSUPPORTED && st != ATTN_ERR_ALIGN) return st;
+  if (Hq < 1 || Hq % Hkv != 0 || Hq > 65535) return ATTN_ERR_SHAPE;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SHAPE;
+  if (st == ATTN_ERR_UNSUPPORTED || Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
+  DecodePlan pl;
+  if (!decode_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return ATTN_ERR_SHAPE;
+  if (!workspace || workspace_bytes < pl.total) return ATTN_ERR_WORKSPACE;
+  if (st == ATTN_ERR_ALIGN || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse))
+    return ATTN_ERR_ALIGN;
+  attn::Decode8Params p{};
+  p.d.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.d.block_table = block_table;
+  p.d.seq_lens = seq_lens;
+  p.d.part_o = static_cast<float*>(workspace);
+  p.d.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.lse_offset);
+  p.d.S = num_seqs;
+  p.d.Hq = Hq;
+  p.d.Hkv = Hkv;
+  p.d.group = Hq / Hkv;
+  p.d.page_size = page_size;
+  p.d.max_pages = max_pages;
+  p.d.num_pages = num_pages;
+  p.d.max_splits = pl.max_splits;
+  p.d.split_tokens = pl.split_tokens;
+  p.d.scale_log2 = scale * kLog2e;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.kv_scales = kv_scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_decode8<128>(p, o, lse, s) : launch_decode8<64>(p, o, lse, s);
+}
+
+}  // extern "C"

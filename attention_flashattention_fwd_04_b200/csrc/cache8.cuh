@@ -1,0 +1,213 @@
+// A paged KV cache in 8 bits: quantising new keys and values as they are
+// written, and reading the cache back.
+//
+// The pools hold e4m3 codes [num_pages, page_size, Hkv, D].  Each row of D
+// values (one token, one KV head) has one power-of-two scale 2^e, kept as a
+// byte e + 127 in kv_scales [num_pages, Hkv, page_size, 2] (the key's, then
+// the value's):
+//     e = the smallest exponent with max|x| <= 448 * 2^e, in [-100, 119]
+//     code = e4m3(x * 2^-e), to nearest even, saturating; the value is code * 2^e.
+// e4m3 is a floating format, so a scale that is not a power of two would round
+// no better; this one is a single byte, its multiplication is exact, and every
+// value of the cache is exact in bf16 (4 significant bits).  The limits keep
+// 2^e and 2^-e normal floats and the largest value, 448 * 2^119, finite; only
+// rows below 2^-91 lose bits to the lower one.
+#pragma once
+
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace attn {
+
+enum : unsigned int {
+  kErrCache8Table = 1u << 14,  // 8-bit cache: a length or block-table entry out of range
+  kErrCache8Wait = 1u << 15,   // 8-bit decode: a pipeline wait ran out
+};
+
+constexpr int kCache8MinExp = -100, kCache8MaxExp = 119;
+
+// The exponent of a row whose largest magnitude is amax (448 = 1.75 * 2^8).
+__device__ __forceinline__ int cache8_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return min(max(e, kCache8MinExp), kCache8MaxExp);
+}
+
+// 2^e for the exponents above and their opposites.
+__device__ __forceinline__ float cache8_pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The sequence that packed row t belongs to: the last s with cu[s] <= t.  All
+// lanes of the warp call it with the same t; 32 candidates a round, so that a
+// thousand sequences take two trips to memory.
+__device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int num_seqs, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = num_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, s < hi && cu[s] <= t));
+    lo += max(below - 1, 0) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+struct Append8Params {
+  const __nv_bfloat16* q;      // [total_q, Hq, D] (with positions only)
+  const __nv_bfloat16* k_new;  // [total_q, Hkv, D]
+  const __nv_bfloat16* v_new;
+  __nv_bfloat16* q_out;
+  uint8_t* k_pool;             // [num_pages, page_size, Hkv, D] e4m3
+  uint8_t* v_pool;
+  uint8_t* kv_scales;          // [num_pages, Hkv, page_size, 2] e8m0
+  const int32_t* positions;    // [axes, total_q]
+  const int32_t* cu_q;         // [num_seqs + 1]
+  const int32_t* seq_lens;     // [num_seqs], after the append
+  const int32_t* block_table;  // [num_seqs, max_pages]
+  int num_seqs, total_q, Hq, Hkv, page_size, max_pages, num_pages;
+};
+
+constexpr int kAppend8Threads = 128;
+
+// One warp a token; lanes as in rope_kernel.  A row's largest magnitude is a
+// reduction over its D / 16 lanes; with ROPE, q and k are turned first and k is
+// quantised from the 32-bit result (one rounding, not two).
+template <int D, bool ROPE>
+__global__ void __launch_bounds__(kAppend8Threads)
+    append8_kernel(const __grid_constant__ RopeTable table, const Append8Params p) {
+  constexpr int kLanes = D / 16;
+  constexpr int kRows = 32 / kLanes;
+  const int t = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  if (t >= p.total_q) return;
+  const int lane = threadIdx.x & 31;
+  const int s = warp_find_sequence(p.cu_q, p.num_seqs, t);
+  const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1], len = p.seq_lens[s];
+  if (t >= q1) return;  // padding behind the last sequence
+  const int nq = q1 - q0;
+  int page = -1, slot = 0;
+  if (t >= q0 && nq <= len && len <= p.max_pages * p.page_size) {
+    const int pos = len - nq + (t - q0);
+    page = p.block_table[static_cast<size_t>(s) * p.max_pages + pos / p.page_size];
+    slot = pos % p.page_size;
+  }
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+    return;
+  }
+  const int l = lane % kLanes;
+  const RopeLane rl = rope_lane(l, ROPE ? table.half : 0, ROPE && table.adjacent);
+  float2 cs[8];
+  if (ROPE && rl.turns) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      cs[i] = rope_cos_sin(p.positions[static_cast<long long>(table.axis[rl.freq + i]) * p.total_q + t],
+                           table.turn[rl.freq + i]);
+  }
+  const int nqh = ROPE ? p.Hq : 0;
+  const int rows = nqh + 2 * p.Hkv;
+  for (int r0 = 0; r0 < rows; r0 += kRows) {
+    const int r = r0 + lane / kLanes;
+    const bool on = r < rows;
+    const bool is_q = r < nqh, is_k = !is_q && r < nqh + p.Hkv;
+    const int h = is_q ? r : is_k ? r - nqh : r - nqh - p.Hkv;
+    const __nv_bfloat16* src = is_q ? p.q + (static_cast<size_t>(t) * p.Hq + h) * D
+                                    : (is_k ? p.k_new : p.v_new) + (static_cast<size_t>(t) * p.Hkv + h) * D;
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (on) {
+      v0 = *reinterpret_cast<const uint4*>(src + rl.off0);
+      v1 = *reinterpret_cast<const uint4*>(src + rl.off1);
+    }
+    float x[8], y[8];
+    unpack_bf16x8(v0, x);
+    unpack_bf16x8(v1, y);
+    if (ROPE && rl.turns && (is_q || is_k)) rope_turn(x, y, cs, table.adjacent);
+    if (is_q) {
+      __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(t) * p.Hq + h) * D;
+      *reinterpret_cast<uint4*>(dst + rl.off0) = rl.turns ? pack_bf16x8(x) : v0;
+      *reinterpret_cast<uint4*>(dst + rl.off1) = rl.turns ? pack_bf16x8(y) : v1;
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (on && !is_q) {
+      const int e = cache8_exponent(amax);
+      const float m = cache8_pow2(-e);
+      uint8_t* dst = (is_k ? p.k_pool : p.v_pool) + ((static_cast<size_t>(page) * p.page_size + slot) * p.Hkv + h) * D;
+      *reinterpret_cast<uint2*>(dst + rl.off0) = make_uint2(pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m),
+                                                            pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
+      *reinterpret_cast<uint2*>(dst + rl.off1) = make_uint2(pack_e4m3x4(y[0] * m, y[1] * m, y[2] * m, y[3] * m),
+                                                            pack_e4m3x4(y[4] * m, y[5] * m, y[6] * m, y[7] * m));
+      if (l == 0)
+        p.kv_scales[((static_cast<size_t>(page) * p.Hkv + h) * p.page_size + slot) * 2 + (is_k ? 0 : 1)] =
+            static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+struct Gather8Params {
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const uint8_t* kv_scales;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_k;         // [num_seqs + 1]: rows of the output
+  __nv_bfloat16* k_out;        // [total_rows, Hkv, D]
+  __nv_bfloat16* v_out;
+  int num_seqs, total_rows, Hkv, page_size, max_pages, num_pages;
+};
+
+constexpr int kGather8Threads = 128;
+
+// Two e4m3 codes times 2^e as a pair of bf16 (exact; NaN codes stay NaN).
+__device__ __forceinline__ uint32_t cache8_bf16x2(uint32_t codes16, float two_e) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes16)));
+  float lo, hi;
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.f32.f16 %0, a;\ncvt.f32.f16 %1, b;\n}\n" : "=f"(lo), "=f"(hi) : "r"(h));
+  return pack_bf16x2(lo * two_e, hi * two_e);
+}
+
+// The scale byte as a float.  0 and 255 are never written (e is limited), but
+// a slot that no token was written to may hold them: such a row's values mean
+// nothing, and 2^-127 or infinity serve as well as any.
+__device__ __forceinline__ float cache8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// One warp a row of the output (one token): 8 codes a lane and step.
+template <int D>
+__global__ void __launch_bounds__(kGather8Threads) gather8_kernel(const Gather8Params p) {
+  const int row = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  if (row >= p.total_rows) return;
+  const int lane = threadIdx.x & 31;
+  const int s = warp_find_sequence(p.cu_k, p.num_seqs, row);
+  const int r0 = p.cu_k[s], r1 = p.cu_k[s + 1], len = p.seq_lens[s];
+  if (row >= r1) return;  // behind the last sequence
+  const int t = row - r0;
+  if (t < 0 || len < 0 || len > p.max_pages * p.page_size || len > r1 - r0) {
+    if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+    return;
+  }
+  if (t >= len) return;  // room behind a sequence: left as it was
+  const int page = p.block_table[static_cast<size_t>(s) * p.max_pages + t / p.page_size];
+  const int slot = t % p.page_size;
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+    return;
+  }
+  const size_t src = (static_cast<size_t>(page) * p.page_size + slot) * p.Hkv * D;
+  const size_t dst = static_cast<size_t>(row) * p.Hkv * D;
+  const uint8_t* scales = p.kv_scales + (static_cast<size_t>(page) * p.Hkv * p.page_size + slot) * 2;
+  for (int i = lane * 8; i < p.Hkv * D; i += 256) {
+    const uint2 k = *reinterpret_cast<const uint2*>(p.k_pool + src + i);
+    const uint2 v = *reinterpret_cast<const uint2*>(p.v_pool + src + i);
+    const uint32_t e = *reinterpret_cast<const uint16_t*>(scales + static_cast<size_t>(i / D) * p.page_size * 2);
+    const float ke = cache8_scale(e & 255u), ve = cache8_scale(e >> 8);
+    *reinterpret_cast<uint4*>(p.k_out + dst + i) = make_uint4(cache8_bf16x2(k.x, ke), cache8_bf16x2(k.x >> 16, ke),
+                                                              cache8_bf16x2(k.y, ke), cache8_bf16x2(k.y >> 16, ke));
+    *reinterpret_cast<uint4*>(p.v_out + dst + i) = make_uint4(cache8_bf16x2(v.x, ve), cache8_bf16x2(v.x >> 16, ve),
+                                                              cache8_bf16x2(v.y, ve), cache8_bf16x2(v.y >> 16, ve));
+  }
+}
+
+}  // namespace attn

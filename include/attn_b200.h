@@ -348,6 +348,131 @@ int paged_prefill_append(const attn_bf16* q, const attn_bf16* k_new, const attn_
                          void* stream);
 
 /*
+ * Rotary positions with several axes.
+ *
+ * attn_rope_spec -- the rotation (HOST memory, read during the call): the
+ * first rot_dim values of every head are rot_dim / 2 pairs; pair j turns by
+ * positions[axis[j]] * inv_freq[j] radians.  The pair is (j, j + rot_dim / 2),
+ * or (2j, 2j + 1) with adjacent_pairs = 1; values behind rot_dim pass through
+ * unchanged.  One axis is the ordinary rotary embedding; images and video use
+ * two or three (height, width; time, height, width), each with its share of the
+ * frequencies in any order.
+ *   rot_dim   a multiple of 16, 16 .. d
+ *   num_axes  1 .. 255
+ *   inv_freq, axis: rot_dim / 2 entries used; finite; axis[j] < num_axes
+ */
+typedef struct attn_rope_spec {
+  int rot_dim;
+  int num_axes;
+  int adjacent_pairs;
+  int reserved; /* 0 */
+  double inv_freq[64];
+  uint8_t axis[64];
+} attn_rope_spec;
+
+/*
+ * attn_rope -- turns the queries and (k, k_out not NULL) the keys of the same
+ * tokens:
+ *     (x, y) -> (x cos a - y sin a, y cos a + x sin a)   for every pair.
+ *   q, q_out   [B, Hq, N, d] bf16, k, k_out [B, Hkv, N, d] bf16, each with its
+ *              strides in elements: {batch, head, token}, host memory, >= 0,
+ *              multiples of 8; the d values of a row are contiguous.  So
+ *              [B, H, N, d], [B, N, H, d] and packed [T, H, d] (B = 1) tensors and
+ *              slices of a fused QKV projection are all taken as they are.
+ *              q_out = q with the same strides works in place; otherwise an output
+ *              overlaps neither the inputs nor the other output, nor itself (an
+ *              output stride is 0 only where its size is 1).
+ *   positions  [num_axes, B, N] int32, any value
+ *   inverse    1 turns by the opposite angle.  The rotation is orthogonal, so
+ *              that is its gradient: dL/dx = attn_rope(dL/dout, inverse = 1).
+ * Angles are exact to 2^-33 turns for every 32-bit position; the rotation runs in
+ * fp32 and is rounded once, to bf16.  d in {64, 128}; B * N = 0 does nothing.
+ * Errors: ATTN_ERR_NULL, ATTN_ERR_SHAPE, ATTN_ERR_ALIGN, ATTN_ERR_LAUNCH.
+ */
+int attn_rope(const attn_bf16* q, attn_bf16* q_out, const long long* q_strides, const long long* q_out_strides, int Hq,
+              const attn_bf16* k, attn_bf16* k_out, const long long* k_strides, const long long* k_out_strides, int Hkv,
+              int B, int N, int d, const int32_t* positions, const attn_rope_spec* spec, int inverse, void* stream);
+
+/*
+ * The paged KV cache in 8 bits: half the memory, and half the bytes a decode
+ * step reads.
+ *
+ *   k_pool, v_pool  [num_pages, page_size, Hkv, d] e4m3 codes (OCP FP8)
+ *   kv_scales       [num_pages, Hkv, page_size, 2] e8m0 exponents (2^(byte - 127)),
+ *                   the key's, then the value's
+ * Each row of d values (one token, one KV head; K and V apart) has its own scale
+ * 2^e, e the smallest exponent in -100 .. 119 with max|x| <= 448 * 2^e, and the
+ * codes are x * 2^-e rounded to nearest even.  Every value, code * 2^e, is exact
+ * in bf16.  Magnitudes above 448 * 2^119, infinities among them, become
+ * 448 * 2^119; NaN stays NaN (and leaves the rest of its row as it would be).
+ * page_size is a multiple of 16, at most 256; d in {64, 128}; the block table,
+ * seq_lens and cu_seqlens_q are those of the bf16 cache.  A length out of range
+ * or a table entry outside the pool is skipped and reported through
+ * attn_device_status (bit 14); nothing is read or written outside the pools.
+ *
+ * paged_kv_append_fp8 -- paged_kv_append into the 8-bit cache: quantises each new
+ * row as it is written.  Rows of k_new / v_new behind cu_seqlens_q[num_seqs] (a
+ * padded batch) and every other slot of the pools and scales stay as they were.
+ * Two new rows of one call must not fall on the same slot.
+ * Errors: ATTN_ERR_NULL, ATTN_ERR_SHAPE, ATTN_ERR_ALIGN, ATTN_ERR_UNSUPPORTED
+ * (page_size), ATTN_ERR_LAUNCH.
+ */
+int paged_kv_append_fp8(const attn_bf16* k_new, const attn_bf16* v_new, uint8_t* k_pool, uint8_t* v_pool, uint8_t* kv_scales,
+                        const int32_t* cu_seqlens_q, const int32_t* seq_lens, const int32_t* block_table, int num_seqs,
+                        int total_q, int Hkv, int d, int page_size, int max_pages, int num_pages, void* stream);
+
+/*
+ * paged_rope_append_fp8 -- attn_rope on a step's q and k_new and
+ * paged_kv_append_fp8, in one kernel: the keys are turned in fp32 and quantised
+ * from there, without a rounding to bf16 between.
+ *   q, q_out   [total_q, Hq, d] bf16, packed as k_new; q_out = q works in place;
+ *              rows of skipped sequences and of padding are not written
+ *   positions  [num_axes, total_q] int32
+ * Errors as above.
+ */
+int paged_rope_append_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, attn_bf16* q_out,
+                          const int32_t* positions, const attn_rope_spec* spec, uint8_t* k_pool, uint8_t* v_pool,
+                          uint8_t* kv_scales, const int32_t* cu_seqlens_q, const int32_t* seq_lens,
+                          const int32_t* block_table, int num_seqs, int total_q, int Hq, int Hkv, int d, int page_size,
+                          int max_pages, int num_pages, void* stream);
+
+/*
+ * paged_kv_gather_fp8 -- reads the 8-bit cache back as bf16 (exact):
+ *   k_out, v_out  [total_rows, Hkv, d] bf16: token t of sequence s goes to row
+ *                 cu_seqlens_k[s] + t, 0 <= t < seq_lens[s]
+ *   cu_seqlens_k  [num_seqs + 1] int32, non-decreasing from 0, at most
+ *                 total_rows; a sequence may have more room than tokens (rows
+ *                 behind its tokens, and behind the last sequence, stay as they
+ *                 were), less is reported and skipped.  With starts rounded up to
+ *                 a page size the output is itself a bf16 pool, which
+ *                 paged_prefill and paged_attn_decode read.
+ * seq_len = 0 is a sequence without tokens.  Errors as above.
+ */
+int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* cu_seqlens_k, attn_bf16* k_out, attn_bf16* v_out,
+                        int num_seqs, int total_rows, int Hkv, int d, int page_size, int max_pages, int num_pages,
+                        void* stream);
+
+/*
+ * paged_attn_decode_fp8 -- paged_attn_decode over the 8-bit cache: the attention
+ * of each sequence's query over the cached values code * 2^e.
+ * q, o, lse, block_table, scale, workspace and the limits (Hq / Hkv <= 16) are
+ * those of paged_attn_decode.  seq_len = 0 (a padded slot of a batch) gives O = 0
+ * and LSE = -inf and is no error; a negative or too long one is reported
+ * (bit 14) with the same outputs; a table entry outside the pool is reported and
+ * leaves its sequence's outputs unspecified.  Scores, softmax statistics and sums
+ * are fp32.  Slots past seq_len, their scales too, may hold anything.
+ * The workspace's contents do not matter; calls that can overlap need one each,
+ * captured graphs that can be replayed at the same time among them.
+ * paged_attn_decode_fp8_workspace_bytes: its size (0 for invalid sizes).
+ */
+size_t paged_attn_decode_fp8_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size);
+int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales,
+                          const int32_t* block_table, const int32_t* seq_lens, int page_size, attn_bf16* o, float* lse,
+                          int num_seqs, int Hq, int Hkv, int d, int max_pages, int num_pages, float scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * attn_device_status -- synchronises `stream`, then reads and clears the
  * device error word of the current device.  Returns ATTN_OK if no kernel
  * recorded an error since the last call, ATTN_ERR_DEVICE otherwise (the raw

@@ -19,3 +19,12 @@ from .attention import (  # noqa: F401
     paged_prefill,
     softmax_with_lse,
 )
+from .cache8 import (  # noqa: F401
+    dequantise,
+    paged_append8,
+    paged_decode8,
+    paged_gather8,
+    pool_values,
+    quantise_rows,
+    rope,
+)
