@@ -3,6 +3,8 @@
 // unit), those of the rotary positions and of the 8-bit paged cache.
 #include "attn_api.cu"
 
+#include <algorithm>
+
 #include "cache8.cuh"
 #include "decode8_sm100.cuh"
 #include "rope.cuh"
@@ -131,15 +133,70 @@ int append8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, 
   return rope ? launch_append8<64, true>(table, p, s) : launch_append8<64, false>(table, p, s);
 }
 
-template <int D>
-int launch_decode8(const attn::Decode8Params& p, attn_bf16* o, float* lse, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.d.max_splits), static_cast<unsigned>(p.d.S), static_cast<unsigned>(p.d.Hq));
-  attn::decode8_split_kernel<D><<<grid, attn::kDecode8Threads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+// The plan of a decode over the 8-bit cache, from the sizes alone: the group of
+// heads a tile covers and the room for partial results.
+struct Decode8Plan {
+  int hb = 0;    // KV heads of a tile
+  int ctas = 0;  // CTAs of the split pass
+  size_t lse_offset = 0, tiles_offset = 0, total = 0;
+};
+
+bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size, Decode8Plan* out) {
+  if (num_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_pages < 1 || page_size < 1 || (d != 64 && d != 128)) return false;
+  const long long max_tokens = static_cast<long long>(max_pages) * page_size;
+  if (max_tokens > INT_MAX) return false;
+  Decode8Plan pl;
+  pl.hb = decode_heads_per_cta(Hkv);
+  const int group = Hq / Hkv;
+  const int tokens = attn::kDecode8Rows / pl.hb;
+  const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
+  // Every CTA that the SMs hold at once (two an SM with up to 8 query heads a
+  // KV head, one with 16), or one a tile.
+  pl.ctas = static_cast<int>(std::min<long long>(tiles, group <= 8 ? 2 * 148 : 148));
+  const size_t rows = 2 * static_cast<size_t>(pl.ctas) * pl.hb * group;
+  pl.lse_offset = rows * d * sizeof(float);
+  pl.tiles_offset = pl.lse_offset + rows * sizeof(float);
+  pl.total = pl.tiles_offset + (attn::kDecode8MaxSeqs + 1) * sizeof(int32_t);
+  pl.total = (pl.total + 15) & ~static_cast<size_t>(15);
+  *out = pl;
+  return true;
+}
+
+// 3-D map of bytes; inner rows of 128 or 64 bytes are swizzled, others not.
+bool encode_3d_bytes(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
+                     uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {stride1, stride2};
+  const cuuint32_t box[3] = {b0, b1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, int STAGES>
+int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& ts, const attn::Decode8Params& p,
+                   cudaStream_t stream) {
+  using L = attn::Decode8Layout<D, STAGES>;
+  auto kernel = attn::decode8_split_kernel<D, NT, STAGES>;
+  cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, STAGES>>(L::kAlloc);
   if (e != cudaSuccess) return fail_cuda(e);
-  const long long warps = static_cast<long long>(p.d.S) * p.d.Hq;
-  const unsigned mgrid = static_cast<unsigned>((warps * 32 + attn::kMergeThreads - 1) / attn::kMergeThreads);
-  attn::decode_merge_kernel<D><<<mgrid, attn::kMergeThreads, 0, stream>>>(p.d, reinterpret_cast<__nv_bfloat16*>(o), lse);
+  kernel<<<static_cast<unsigned>(p.ctas), attn::kDecode8Threads, L::kAlloc, stream>>>(tk, tv, ts, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.Hq), static_cast<unsigned>(p.S));
+  cfg.blockDim = dim3(attn::kMerge8Threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D>, p);
+  if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
 }
@@ -239,8 +296,8 @@ int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint
 }
 
 size_t paged_attn_decode_fp8_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size) {
-  DecodePlan pl;
-  if (Hkv < 1 || !decode_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return 0;
+  Decode8Plan pl;
+  if (!decode8_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return 0;
   return pl.total;
 }
 
@@ -255,32 +312,54 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
   if (Hq < 1 || Hq % Hkv != 0 || Hq > 65535) return ATTN_ERR_SHAPE;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_SHAPE;
   if (st == ATTN_ERR_UNSUPPORTED || Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
-  DecodePlan pl;
-  if (!decode_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return ATTN_ERR_SHAPE;
+  Decode8Plan pl;
+  if (!decode8_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return ATTN_ERR_SHAPE;
   if (!workspace || workspace_bytes < pl.total) return ATTN_ERR_WORKSPACE;
   if (st == ATTN_ERR_ALIGN || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse))
     return ATTN_ERR_ALIGN;
+
+  CUtensorMap tk, tv, ts;
+  const uint64_t rows = static_cast<uint64_t>(num_pages) * page_size;
+  const uint64_t token_bytes = static_cast<uint64_t>(Hkv) * d;
+  const uint32_t hb = static_cast<uint32_t>(pl.hb);
+  const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  // Codes: (value, token row, head), a box the 16 tokens of HB heads; scales:
+  // (slot and K or V, head, page), the same tokens' 32 bytes a head.
+  if (!encode_3d_bytes(&tk, k_pool, d, rows, Hkv, token_bytes, d, d, 16, hb, sw) ||
+      !encode_3d_bytes(&tv, v_pool, d, rows, Hkv, token_bytes, d, d, 16, hb, sw) ||
+      !encode_3d_bytes(&ts, kv_scales, 2 * static_cast<uint64_t>(page_size), Hkv, num_pages, 2 * static_cast<uint64_t>(page_size),
+                       2 * static_cast<uint64_t>(page_size) * Hkv, 32, hb, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return fail_cuda(cudaErrorInvalidValue);
+
   attn::Decode8Params p{};
-  p.d.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.d.block_table = block_table;
-  p.d.seq_lens = seq_lens;
-  p.d.part_o = static_cast<float*>(workspace);
-  p.d.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.lse_offset);
-  p.d.S = num_seqs;
-  p.d.Hq = Hq;
-  p.d.Hkv = Hkv;
-  p.d.group = Hq / Hkv;
-  p.d.page_size = page_size;
-  p.d.max_pages = max_pages;
-  p.d.num_pages = num_pages;
-  p.d.max_splits = pl.max_splits;
-  p.d.split_tokens = pl.split_tokens;
-  p.d.scale_log2 = scale * kLog2e;
-  p.k_pool = k_pool;
-  p.v_pool = v_pool;
-  p.kv_scales = kv_scales;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.lse_offset);
+  p.first_tile = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + pl.tiles_offset);
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.group = Hq / Hkv;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.hb = pl.hb;
+  p.ctas = pl.ctas;
+  p.scale_log2 = scale * kLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_decode8<128>(p, o, lse, s) : launch_decode8<64>(p, o, lse, s);
+  for (int s0 = 0; s0 < num_seqs; s0 += attn::kDecode8MaxSeqs) {  // one launch for up to 1024 sequences
+    p.S = std::min(num_seqs - s0, attn::kDecode8MaxSeqs);
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q) + static_cast<size_t>(s0) * Hq * d;
+    p.o = reinterpret_cast<__nv_bfloat16*>(o) + static_cast<size_t>(s0) * Hq * d;
+    p.lse = lse + static_cast<size_t>(s0) * Hq;
+    p.block_table = block_table + static_cast<size_t>(s0) * max_pages;
+    p.seq_lens = seq_lens + s0;
+    int rc;
+    if (d == 128)
+      rc = p.group <= 8 ? launch_decode8<128, 1, 3>(tk, tv, ts, p, s) : launch_decode8<128, 2, 6>(tk, tv, ts, p, s);
+    else
+      rc = p.group <= 8 ? launch_decode8<64, 1, 6>(tk, tv, ts, p, s) : launch_decode8<64, 2, 10>(tk, tv, ts, p, s);
+    if (rc != ATTN_OK) return rc;
+  }
+  return ATTN_OK;
 }
 
 }  // extern "C"

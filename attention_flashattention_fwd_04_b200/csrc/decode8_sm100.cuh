@@ -1,95 +1,611 @@
-// Paged decode over the 8-bit cache (cache8.cuh): one new token a sequence,
-// split over the cache's length and joined by decode_merge_kernel.
+// Paged decode over the 8-bit cache (cache8.cuh): one new token a sequence.
 //     s_t = scale * 2^ek_t * (q . kc_t),  O = sum_t softmax(s)_t 2^ev_t vc_t
 // with kc, vc the codes of token t's key and value and ek, ev their exponents.
+//
+// Bound by the read of the cache.  The work is the tiles of 128 cached rows
+// (16 tokens of 8 KV heads, or 128 / HB tokens of HB heads), in order of
+// sequence, group of heads, position; every CTA takes an equal run of them,
+// whatever the sequences' lengths (they are read and summed up on the device),
+// so that all SMs finish together.  A run that covers the whole of a sequence's
+// tiles writes its output; others write partial results, at most two a CTA,
+// which decode8_merge_kernel joins.
+//
+// A producer warp brings tiles by TMA (codes and scales) into a ring; warp w of
+// the 8 consumers works on the tile's rows 16 w .. 16 w + 15, 16 tokens of one
+// head.  Both products run on mma.sync m16n8k16 with the cache as the 16-row
+// operand and the query heads of the group as the 8 columns (tcgen05's tiles
+// are far larger than a group of query heads, and there are a few FLOP per
+// byte): S^T = K Q^T and O^T += V^T P^T.
+//   - e4m3 codes become f16 exactly; q, scaled by a power of two of its row to
+//     use f16's range, keeps its 8 bits (values 2^-28 below the row's largest
+//     and less lose some).
+//   - V's scale goes into the weights before they are rounded:
+//     p_t = 2^(s_t + ev_t - m), m a running bound of s_t + ev_t, so that no
+//     weight overflows f16 however far apart the scales are; it is 2^8 off the
+//     largest at most, and the stored weight has 11 bits down to 2^-20 of m.
+//     The softmax's own sum takes 2^(s_t - m) in fp32.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "cache8.cuh"
 #include "decode_sm100.cuh"
 
 namespace attn {
 
+constexpr int kDecode8Warps = 8;                           // consumers
+constexpr int kDecode8Threads = 32 * (kDecode8Warps + 1);  // and the producer
+constexpr int kDecode8Rows = 16 * kDecode8Warps;           // cached rows of a tile
+constexpr int kDecode8MaxSeqs = 1024;                      // sequences of one launch
+
 struct Decode8Params {
-  DecodeParams d;
-  const uint8_t* k_pool;
-  const uint8_t* v_pool;
-  const uint8_t* kv_scales;
+  const __nv_bfloat16* q;      // [S, Hq, D]
+  const int32_t* block_table;  // [S, max_pages]
+  const int32_t* seq_lens;     // [S]
+  __nv_bfloat16* o;            // [S, Hq, D]
+  float* lse;                  // [S, Hq]
+  int32_t* first_tile;         // workspace [S + 1]: tiles before each sequence, of one group of heads
+  float* part_lse;             // workspace [2 ctas, HB * group], in log2
+  float* part_o;               // workspace [2 ctas, HB * group, D]
+  int S, Hq, Hkv, group, page_size, max_pages, num_pages, hb, ctas;
+  float scale_log2;
 };
 
-constexpr int kDecode8Threads = 128;
+template <int D, int STAGES>
+struct Decode8Layout {
+  static constexpr int kPool = kDecode8Rows * D;          // codes of K (or V) of one tile
+  static constexpr int kScales = 1024;                    // 32 bytes a warp; a chunk's start on 128 bytes
+  static constexpr int kStage = 2 * kPool + kScales;
+  static constexpr int kBar = STAGES * kStage;
+  static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
+  static constexpr int kJoin = kWarpSums + kDecode8Warps * 4;  // the warps' bounds and sums, where they join
+  static constexpr int kJoinBytes = 2 * kDecode8Warps * 16 * 4;
+  static constexpr int kJoinRows = kJoin + kJoinBytes;         // 16 bytes a lane
+  static constexpr int kTiles = kJoinRows + kDecode8Warps * 512;
+  static constexpr int kBytes = kTiles + (kDecode8MaxSeqs + 1) * 4;
+  static constexpr int kAlloc = kBytes + 1024;
+};
 
-// CTA (split, sequence, query head): each warp takes every fourth token of the
-// split with its own running maximum and sum; the four are joined at the end.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held one row pair a lane.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two e4m3 codes (the low or high half of w) as f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(h) : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, b;\n}\n" : "=r"(h) : "r"(w));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint4 lds_128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte vector `c` of row `r` in a warp's 16 x D tile, as TMA
+// swizzles it: 128-byte rows XOR the vector with r % 8, 64-byte rows with
+// (r / 2) % 4.
 template <int D>
-__global__ void __launch_bounds__(kDecode8Threads) decode8_split_kernel(const Decode8Params p) {
-  constexpr int kPer = D / 32;
-  constexpr int kWarps = kDecode8Threads / 32;
-  __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
-  const DecodeParams& d = p.d;
-  const int split = blockIdx.x, s = blockIdx.y, h = blockIdx.z;
+__device__ __forceinline__ uint32_t decode8_offset(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void decode8_consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecode8Warps) : "memory");
+}
+
+// The tiles [from, to) of sequence s and head group hg, out of n.
+struct Decode8Run {
+  int s, hg, from, to, n;
+};
+
+// The run that begins at tile `at` of all, cut at `end`.  first: first_tile in
+// shared memory.
+__device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, int groups, long long at, long long end) {
+  int lo = 0, hi = S;  // the last sequence that begins at or before tile `at`: it is not empty, since at < total
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<long long>(first[mid]) * groups <= at) lo = mid; else hi = mid;
+  }
+  Decode8Run r;
+  r.s = lo;
+  r.n = first[lo + 1] - first[lo];
+  const long long in = at - static_cast<long long>(first[lo]) * groups;
+  r.hg = static_cast<int>(in / r.n);
+  r.from = static_cast<int>(in % r.n);
+  r.to = static_cast<int>(min(static_cast<long long>(r.n), r.from + (end - at)));
+  return r;
+}
+
+// One tile for one warp.
+template <int D, int NT>
+struct Decode8Warp {
+  float acc[NT][D / 16][4];  // O^T: values 16 c + 2 grp (+ 1) of heads 2 tig (+ 1)
+  float m[NT][2], l[NT][2];  // of heads 2 tig (+ 1); l is this lane's share
+  float f[NT][2];            // scores' factor
+  uint32_t q[NT][D / 16][2];
+
+  __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + grp;
+      uint2 raw[D / 16];
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        // Step i of the product takes values 4 (i % 4) .. + 3 of 16-byte vector
+        // (D / 64) tig + i / 4 of a key row: the same values of q.
+        const int c = (D / 64) * tig + i / 4;
+        raw[i] = make_uint2(0u, 0u);
+        if (h < group) raw[i] = *reinterpret_cast<const uint2*>(qrow + h * D + 16 * c + 4 * (i % 4));
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(__uint_as_float(raw[i].x << 16)), fabsf(__uint_as_float(raw[i].x & 0xffff0000u))),
+                                 fmaxf(fabsf(__uint_as_float(raw[i].y << 16)), fabsf(__uint_as_float(raw[i].y & 0xffff0000u)))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // Largest magnitude to 2^13 .. 2^14 (as far as 2^shift is a normal float).
+      int shift = 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
+      shift = amax == 0.f || amax > 3.4e38f ? 0 : min(shift, 126);
+      const float up = __int_as_float((shift + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        q[nt][i][0] = pack_f16x2(__uint_as_float(raw[i].x << 16) * up, __uint_as_float(raw[i].x & 0xffff0000u) * up);
+        q[nt][i][1] = pack_f16x2(__uint_as_float(raw[i].y << 16) * up, __uint_as_float(raw[i].y & 0xffff0000u) * up);
+      }
+      const float factor = scale_log2 * __int_as_float((127 - shift) << 23);  // of head grp; wanted: of heads 2 tig (+ 1)
+      f[nt][0] = __shfl_sync(0xffffffffu, factor, 8 * tig);
+      f[nt][1] = __shfl_sync(0xffffffffu, factor, 8 * tig + 4);
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
+    }
+  }
+
+  // valid: the tokens of the 16 that belong to the sequence (TAIL: fewer than 16).
+  template <bool TAIL>
+  __device__ __forceinline__ void tile(uint32_t k, uint32_t v, uint32_t scales, int valid, int lane) {
+    const int grp = lane >> 2, tig = lane & 3;
+    float sc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const int c = (D / 64) * tig + j;
+      const uint4 ka = lds_128(k + decode8_offset<D>(grp, c)), kb = lds_128(k + decode8_offset<D>(grp + 8, c));
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = e4m3x2_f16x2_lo(wa[i]), a1 = e4m3x2_f16x2_lo(wb[i]);
+        const uint32_t a2 = e4m3x2_f16x2_hi(wa[i]), a3 = e4m3x2_f16x2_hi(wb[i]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt], a0, a1, a2, a3, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
+      }
+    }
+    const uint32_t e0 = lds_u16(scales + 2 * grp), e1 = lds_u16(scales + 2 * grp + 16);
+    const float k0 = cache8_scale(e0 & 255u), k1 = cache8_scale(e1 & 255u);
+    const float v0 = static_cast<float>(static_cast<int>(e0 >> 8) - 127), v1 = static_cast<float>(static_cast<int>(e1 >> 8) - 127);
+    bool up = false;
+    float t[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool out = TAIL && grp + 8 * (e >> 1) >= valid;
+        sc[nt][e] = out ? -INFINITY : sc[nt][e] * ((e < 2 ? k0 : k1) * f[nt][e & 1]);
+        t[nt][e] = out ? -INFINITY : sc[nt][e] + (e < 2 ? v0 : v1);
+        up |= t[nt][e] > m[nt][e & 1] + 8.f;
+      }
+    }
+    if (__any_sync(0xffffffffu, up)) {  // a new bound: the largest so far
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float mx = fmaxf(t[nt][u], t[nt][u + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx, m[nt][u]);
+          const float a = ex2_approx(m[nt][u] - mx);
+          m[nt][u] = mx;
+          l[nt][u] *= a;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            acc[nt][c][u] *= a;
+            acc[nt][c][u + 2] *= a;
+          }
+        }
+      }
+    }
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = ex2_approx(t[nt][e] - m[nt][e & 1] + 6.f);
+      l[nt][0] += ex2_approx(sc[nt][0] - m[nt][0]) + ex2_approx(sc[nt][2] - m[nt][0]);
+      l[nt][1] += ex2_approx(sc[nt][1] - m[nt][1]) + ex2_approx(sc[nt][3] - m[nt][1]);
+      p[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+      p[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+    }
+    // Tokens past the end may hold NaN codes, and 0 * NaN is NaN: their codes
+    // are cleared (token 2 tig in the low half of a word, 2 tig + 1 in the high).
+    const uint32_t keep0 = (2 * tig < valid ? 0xffffu : 0u) | (2 * tig + 1 < valid ? 0xffff0000u : 0u);
+    const uint32_t keep1 = (2 * tig + 8 < valid ? 0xffffu : 0u) | (2 * tig + 9 < valid ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      // Matrices: tokens 0-7 and 8-15 of vector c, then of vector c + 1.  Each
+      // 16-bit element is two codes (d, d + 1) of one token; transposed, a lane
+      // holds them for tokens 2 tig and 2 tig + 1, and bytes 1 and 2 change
+      // places so that each half is one d of both tokens.
+      uint32_t r[4];
+      const int row = (lane & 7) + (lane & 8), col = c + (lane >> 4);
+      ldmatrix_x4_trans(v + decode8_offset<D>(row, col), r[0], r[1], r[2], r[3]);
+      if (TAIL) {
+        r[0] &= keep0;
+        r[1] &= keep1;
+        r[2] &= keep0;
+        r[3] &= keep1;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t x = __byte_perm(r[2 * u], 0u, 0x3120), y = __byte_perm(r[2 * u + 1], 0u, 0x3120);
+        const uint32_t a0 = e4m3x2_f16x2_lo(x), a1 = e4m3x2_f16x2_hi(x);
+        const uint32_t a2 = e4m3x2_f16x2_lo(y), a3 = e4m3x2_f16x2_hi(y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][c + u], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+      }
+    }
+  }
+};
+
+template <int D, int NT, int STAGES>
+__global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
+    decode8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_s, const Decode8Params p) {
+  using L = Decode8Layout<D, STAGES>;
+  // The merge may be launched once every CTA has begun; it waits for this grid.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  auto full_bar = [&](int st) -> uint32_t { return base + L::kBar + 8u * st; };
+  auto empty_bar = [&](int st) -> uint32_t { return base + L::kBar + 8u * (STAGES + st); };
+  int32_t* first = reinterpret_cast<int32_t*>(smem + L::kTiles);
+  int32_t* warp_sums = reinterpret_cast<int32_t*>(smem + L::kWarpSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seq_len = d.seq_lens[s];
-  if (seq_len < 0 || seq_len > d.max_pages * d.page_size) {
-    if (split == 0 && h == 0 && threadIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
-    return;
-  }
-  const int begin = split * d.split_tokens, end = min(seq_len, begin + d.split_tokens);
-  if (begin >= end) return;
-  const int hk = h / d.group;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = __bfloat162float(d.q[(static_cast<size_t>(s) * d.Hq + h) * D + lane * kPer + i]) * d.scale_log2;
-    o[i] = 0.f;
-  }
-  for (int t = begin + warp; t < end; t += kWarps) {
-    int page = d.block_table[static_cast<size_t>(s) * d.max_pages + t / d.page_size];
-    if (page < 0 || page >= d.num_pages) {
-      if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
-      page = 0;
+  const int tokens = kDecode8Rows / p.hb;  // of a tile
+
+  // Tiles before each sequence: every consumer thread sums up a run of
+  // lengths, the warps' sums follow.
+  const int per = (p.S + 32 * kDecode8Warps - 1) / (32 * kDecode8Warps);
+  int own = 0, before = 0;
+  if (warp < kDecode8Warps) {
+    for (int i = 0; i < per; ++i) {
+      const int s = threadIdx.x * per + i;
+      if (s >= p.S) break;
+      int len = p.seq_lens[s];
+      if (len < 0 || len > p.max_pages * p.page_size) {
+        if (blockIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+        len = 0;
+      }
+      own += (len + tokens - 1) / tokens;
+      first[s + 1] = own;
     }
-    const int slot = t % d.page_size;
-    const size_t at = ((static_cast<size_t>(page) * d.page_size + slot) * d.Hkv + hk) * D + lane * kPer;
-    const uint8_t* e = p.kv_scales + ((static_cast<size_t>(page) * d.Hkv + hk) * d.page_size + slot) * 2;
-    const float ke = cache8_scale(e[0]), ve = cache8_scale(e[1]);
-    float dot = 0.f;
-    float v[kPer];
+    before = own;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      uint32_t kc = cache8_bf16x2(*reinterpret_cast<const uint16_t*>(p.k_pool + at + i), 1.f);
-      uint32_t vc = cache8_bf16x2(*reinterpret_cast<const uint16_t*>(p.v_pool + at + i), 1.f);
-      dot += q[i] * __uint_as_float(kc << 16) + q[i + 1] * __uint_as_float(kc & 0xffff0000u);
-      v[i] = __uint_as_float(vc << 16) * ve;
-      v[i + 1] = __uint_as_float(vc & 0xffff0000u) * ve;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, before, off);
+      if (lane >= off) before += x;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    dot *= ke;
-    const float mn = fmaxf(m, dot);
-    const float a = exp2f(m - mn), w = exp2f(dot - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = o[i] * a + w * v[i];
+    if (lane == 31) warp_sums[warp] = before;
+    before -= own;
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) so[warp][lane * kPer + i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+  if (threadIdx.x == 0) {
+    first[0] = 0;
+    for (int st = 0; st < STAGES; ++st) {
+      mbar_init(full_bar(st), 1);
+      mbar_init(empty_bar(st), kDecode8Warps);
+    }
+    fence_mbar_init();
   }
   __syncthreads();
-  float mx = sm[0];
-  for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm[w]);
-  float total = 0.f;
-  for (int w = 0; w < kWarps; ++w) total += sl[w] * exp2f(sm[w] - mx);
-  const size_t row = (static_cast<size_t>(s) * d.Hq + h) * d.max_splits + split;
-  for (int i = threadIdx.x; i < D; i += kDecode8Threads) {
-    float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) sum += so[w][i] * exp2f(sm[w] - mx);
-    d.part_o[row * D + i] = sum / total;
+  if (warp < kDecode8Warps) {
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    for (int i = 0; i < per; ++i) {
+      const int s = threadIdx.x * per + i;
+      if (s < p.S) first[s + 1] += before;
+    }
   }
-  if (threadIdx.x == 0) d.part_lse[row] = (mx + log2f(total)) * 0.69314718055994530942f;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s <= p.S; s += kDecode8Threads) p.first_tile[s] = first[s];
+
+  const int groups = p.Hkv / p.hb;
+  const long long total = static_cast<long long>(first[p.S]) * groups;
+  const long long ctas = min(static_cast<long long>(p.ctas), total);
+  if (static_cast<long long>(blockIdx.x) >= ctas) return;
+  const long long begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
+
+  if (warp == kDecode8Warps) {
+    // ------------------------------------------------------------ producer
+    const int chunks_per_tile = kDecode8Warps / p.hb;  // chunks of 16 tokens, one lane each
+    const uint32_t scale_stride = max(128, 32 * p.hb);
+    const uint32_t chunk_bytes = p.hb * 16 * (2 * D + 2);
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_s);
+    }
+    bool ok = true;
+    int count = 0;  // tiles issued
+    for (long long at = begin; at < end && ok;) {
+      const Decode8Run run = decode8_run(first, p.S, groups, at, end);
+      at += run.to - run.from;
+      const int len = p.seq_lens[run.s];
+      const int chunk_end = min((len + 15) / 16, run.to * chunks_per_tile);
+      const int32_t* table = p.block_table + static_cast<size_t>(run.s) * p.max_pages;
+      // Pages of 32 chunks at a time, one a lane; the next 32 are under way
+      // while these are used.
+      int window = run.from * chunks_per_tile;
+      auto fetch = [&](int c) { return c < chunk_end ? table[c * 16 / p.page_size] : 0; };
+      int page = fetch(window + lane), next = fetch(window + 32 + lane);
+      for (int tile = run.from; tile < run.to; ++tile, ++count) {
+        const int c0 = tile * chunks_per_tile;
+        if (c0 >= window + 32) {
+          window += 32;
+          page = next;
+          next = fetch(window + 32 + lane);
+        }
+        int pg = __shfl_sync(0xffffffffu, page, (c0 - window + lane) & 31);
+        const int n = min(chunks_per_tile, chunk_end - c0);
+        const int st = count % STAGES, round = count / STAGES;
+        if (round > 0) ok = mbar_wait(empty_bar(st), (round - 1) & 1u, kErrCache8Wait);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), n * chunk_bytes);
+        __syncwarp();
+        if (lane < n) {
+          if (pg < 0 || pg >= p.num_pages) {
+            atomicOr(&g_attn_device_error, kErrCache8Table);
+            pg = 0;  // keeps every copy inside the pool; the result is flagged
+          }
+          const int slot = (c0 + lane) * 16 % p.page_size;
+          const uint32_t dst = base + st * L::kStage;
+          const int row = pg * p.page_size + slot, head = run.hg * p.hb;
+          tma_load_3d(dst + lane * p.hb * 16 * D, &tm_k, full_bar(st), 0, row, head);
+          tma_load_3d(dst + 2 * L::kPool + lane * scale_stride, &tm_s, full_bar(st), 2 * slot, head, pg);
+          tma_load_3d(dst + L::kPool + lane * p.hb * 16 * D, &tm_v, full_bar(st), 0, row, head);
+        }
+        __syncwarp();
+      }
+    }
+    // No copy may be in flight when the CTA ends.
+    for (int c = max(0, count - STAGES); c < count; ++c)
+      mbar_wait(full_bar(c % STAGES), static_cast<uint32_t>(c / STAGES) & 1u, kErrCache8Wait);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int grp = lane >> 2, tig = lane & 3;
+  const int hl = warp % p.hb, chunk = warp / p.hb, parts = kDecode8Warps / p.hb;
+  const uint32_t scale_at = 2 * L::kPool + chunk * max(128, 32 * p.hb) + hl * 32;
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [2][warp][16 heads]
+  float4* join_rows = reinterpret_cast<float4*>(smem + L::kJoinRows);  // [warp][lane]
+  int count = 0;
+  bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
+  for (long long at = begin; at < end;) {
+    const Decode8Run run = decode8_run(first, p.S, groups, at, end);
+    at += run.to - run.from;
+    const int len = p.seq_lens[run.s];
+    const int hk = run.hg * p.hb + hl;
+    const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(hk) * p.group;
+    Decode8Warp<D, NT> w;
+    w.begin(p.q + head0 * D, p.group, p.scale_log2, grp, tig);
+    for (int tile = run.from; tile < run.to; ++tile, ++count) {
+      const int st = count % STAGES;
+      if (ok) ok = mbar_wait(full_bar(st), static_cast<uint32_t>(count / STAGES) & 1u, kErrCache8Wait);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      const uint32_t k = base + st * L::kStage + warp * 16 * D, v = k + L::kPool, sc = base + st * L::kStage + scale_at;
+      const int valid = len - tile * tokens - chunk * 16;
+      if (valid >= 16)
+        w.template tile<false>(k, v, sc, 16, lane);
+      else if (valid > 0)
+        w.template tile<true>(k, v, sc, valid, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(st));
+    }
+    // Sums over the lanes that share a head.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) w.l[nt][u] += __shfl_xor_sync(0xffffffffu, w.l[nt][u], off);
+    if (parts > 1) {
+      // The warps of one head hold different tokens.
+      if (grp == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            join[warp * 16 + nt * 8 + 2 * tig + u] = w.m[nt][u];
+            join[kDecode8Warps * 16 + warp * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
+          }
+      }
+      decode8_consumers_sync();
+    }
+    // Bound and sum of the head over its warps, and this warp's share of O.
+    const bool whole = run.from == 0 && run.to == run.n;
+    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0);
+    const int rows = p.hb * p.group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = nt * 8 + 2 * tig + u;
+        float mx = w.m[nt][u], sum = w.l[nt][u];
+        if (parts > 1) {  // (the barriers of the rows' join below keep the next run from overwriting these)
+          mx = -INFINITY;
+          for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[(i * p.hb + hl) * 16 + h]);
+          sum = 0.f;
+          for (int i = 0; i < parts; ++i)
+            sum += join[kDecode8Warps * 16 + (i * p.hb + hl) * 16 + h] * ex2_approx(join[(i * p.hb + hl) * 16 + h] - mx);
+        }
+        // O = acc * 2^(m - mx - 6) / sum
+        const float a = ex2_approx(w.m[nt][u] - mx - 6.f) / sum;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          w.acc[nt][c][u] *= a;
+          w.acc[nt][c][u + 2] *= a;
+        }
+        if (chunk == 0 && grp == 0 && h < p.group) {
+          const float lse2 = mx + log2f(sum);
+          if (whole)
+            p.lse[head0 + h] = lse2 * 0.69314718055994530942f;
+          else
+            p.part_lse[slot * rows + hl * p.group + h] = lse2;
+        }
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        if (parts > 1) {
+          // The head's first warp adds up the others', in their order.
+          join_rows[threadIdx.x] = make_float4(w.acc[nt][c][0], w.acc[nt][c][1], w.acc[nt][c][2], w.acc[nt][c][3]);
+          decode8_consumers_sync();
+          if (chunk == 0) {
+            for (int i = 1; i < parts; ++i) {
+              const float4 x = join_rows[(i * p.hb + hl) * 32 + lane];
+              w.acc[nt][c][0] += x.x;
+              w.acc[nt][c][1] += x.y;
+              w.acc[nt][c][2] += x.z;
+              w.acc[nt][c][3] += x.w;
+            }
+          }
+          decode8_consumers_sync();
+        }
+        const int d = 16 * c + 2 * grp;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int h = nt * 8 + 2 * tig + u;
+          if (chunk != 0 || h >= p.group) continue;
+          if (whole)
+            *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + d) = pack_bf16x2(w.acc[nt][c][u], w.acc[nt][c][u + 2]);
+          else
+            *reinterpret_cast<float2*>(p.part_o + (slot * rows + hl * p.group + h) * D + d) =
+                make_float2(w.acc[nt][c][u], w.acc[nt][c][u + 2]);
+        }
+      }
+  }
+}
+
+constexpr int kMerge8Threads = 128;
+
+// Joins the partial results of one sequence and query head, a CTA each:
+//     lse = log sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
+// Which CTAs hold them follows from first_tile as in the split pass; heads that
+// one CTA held alone are written already.  Each of the 4 warps adds up every
+// fourth partial row, and the four are added in their order.
+template <int D>
+__global__ void __launch_bounds__(kMerge8Threads) decode8_merge_kernel(const Decode8Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kWarps = kMerge8Threads / 32, kPer = D / 32;
+  __shared__ float rows[kWarps][D];
+  const int h = blockIdx.x, s = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int a0 = p.first_tile[s], n = p.first_tile[s + 1] - a0;
+  const size_t head = static_cast<size_t>(s) * p.Hq + h;
+  if (n == 0) {  // no tokens (or a length that the split pass reported)
+    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(p.o + head * D)[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) p.lse[head] = -INFINITY;
+    return;
+  }
+  const int groups = p.Hkv / p.hb, hk = h / p.group;
+  const long long total = static_cast<long long>(p.first_tile[p.S]) * groups;
+  const long long ctas = min(static_cast<long long>(p.ctas), total);
+  const long long at = static_cast<long long>(a0) * groups + static_cast<long long>(hk / p.hb) * n;
+  // CTA c begins at tile c * total / ctas.
+  const int c0 = static_cast<int>(((at + 1) * ctas - 1) / total), c1 = static_cast<int>(((at + n) * ctas - 1) / total);
+  const int pieces = c1 - c0 + 1;
+  if (pieces == 1) return;
+  const int per_slot = p.hb * p.group, row0 = (hk % p.hb) * p.group + h % p.group;
+  auto row_of = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * per_slot + row0; };
+  float mx = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, p.part_lse[row_of(i)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  float sum = 0.f;
+  for (int i = lane; i < pieces; i += 32) sum += ex2_approx(p.part_lse[row_of(i)] - mx);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  float out[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) out[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < pieces; i += kWarps) {
+    const size_t row = row_of(i);
+    const float w = ex2_approx(p.part_lse[row] - mx);
+    const float* src = p.part_o + row * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      out[0] = fmaf(w, x.x, out[0]);
+      out[1] = fmaf(w, x.y, out[1]);
+      out[2] = fmaf(w, x.z, out[2]);
+      out[3] = fmaf(w, x.w, out[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      out[0] = fmaf(w, x.x, out[0]);
+      out[1] = fmaf(w, x.y, out[1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) rows[warp][lane * kPer + e] = out[e];
+  __syncthreads();
+  const float inv = 1.f / sum;
+  if (threadIdx.x < D / 2) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      x += rows[w][2 * threadIdx.x];
+      y += rows[w][2 * threadIdx.x + 1];
+    }
+    reinterpret_cast<uint32_t*>(p.o + head * D)[threadIdx.x] = pack_bf16x2(x * inv, y * inv);
+  }
+  if (threadIdx.x == 0) p.lse[head] = (mx + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace attn

@@ -283,3 +283,48 @@ def test_python_rope_refusals():
         api.attn_rope(q.float(), None, pos, spec)
     with pytest.raises(TypeError):
         api.attn_rope(q, None, pos, object())
+
+
+# ------------------------------------------------- the decode's share-out of work
+
+@pytest.mark.parametrize("seed", range(6))
+def test_decode_share_out(seed):
+    """The split pass's runs and the merge's pieces, in their own arithmetic: every tile falls to one run, a CTA writes at most
+    one partial result to each of its two slots, and the merge reads exactly the slots that were written."""
+    rng = np.random.default_rng(seed)
+    for _ in range(60):
+        S, groups = int(rng.integers(1, 20)), int(rng.integers(1, 5))
+        first = np.concatenate([[0], np.cumsum(rng.integers(0, 30, S) * (rng.random(S) < 0.8))]).astype(int)
+        total = int(first[-1]) * groups
+        ctas = min(int(rng.integers(1, 60)), total)
+        seen, slots = set(), {}
+        for c in range(ctas):
+            at, end = c * total // ctas, (c + 1) * total // ctas
+            assert at < end
+            while at < end:
+                lo, hi = 0, S
+                while hi - lo > 1:
+                    mid = (lo + hi) // 2
+                    lo, hi = (mid, hi) if first[mid] * groups <= at else (lo, mid)
+                n = int(first[lo + 1] - first[lo])
+                assert n > 0
+                hg, a = divmod(at - int(first[lo]) * groups, n)
+                b = min(n, a + end - at)
+                for t in range(a, b):
+                    assert (lo, hg, t) not in seen
+                    seen.add((lo, hg, t))
+                if not (a == 0 and b == n):
+                    slot = 2 * c + (1 if a == 0 else 0)
+                    assert slot not in slots
+                    slots[slot] = (lo, hg)
+                at += b - a
+        assert len(seen) == total
+        read = {}
+        for s in range(S):
+            n = int(first[s + 1] - first[s])
+            for hg in range(groups if n else 0):
+                at = int(first[s]) * groups + hg * n
+                c0, c1 = ((at + 1) * ctas - 1) // total, ((at + n) * ctas - 1) // total
+                if c1 > c0:
+                    read.update({2 * (c0 + i) + (1 if i == 0 else 0): (s, hg) for i in range(c1 - c0 + 1)})
+        assert read == slots
