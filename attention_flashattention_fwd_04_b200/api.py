@@ -8,6 +8,7 @@ the library is missing or a call fails, this module raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -663,29 +664,32 @@ def rope_spec(d: int, sections=None, theta: float = 10000.0, rot_dim: int | None
     return spec
 
 
-def _one_device(**tensors):
+def _one_device(tensors, names):
     """Checks, after the shapes, that the tensors (None left out) are on one
-    CUDA device; returns it."""
-    device = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if device is None:
-            device = t.device
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return device
+    CUDA device; returns its index."""
+    index = tensors[0].get_device()
+    for t, name in zip(tensors, names):
+        if t is not None and (t.get_device() != index or index < 0):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, not on {tensors[0].device}")
+    return index
 
 
-def _launch_stream(stream, device):
-    """The stream of a call: the current one of ``device``, or the given one, which must be a stream of it."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stream
+_HERE = contextlib.nullcontext()
+
+
+def _launch_on(index, stream):
+    """(context, stream handle) of a call on device ``index``: the given
+    stream, which must be one of that device, or its current stream.  What the
+    call allocates inside the context belongs to that stream, so that it is not
+    handed out again while the call may still use it."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    here = _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return here, torch.cuda.current_stream(index).cuda_stream
 
 
 def _rope_tensor(x, name, out, out_name):
@@ -736,9 +740,8 @@ def attn_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, 
     _require(positions, "positions", torch.int32, 1 + len(where), cuda=False)
     if positions.shape != (spec.num_axes, *where):
         raise ValueError(f"positions must be {(spec.num_axes, *where)}, got {tuple(positions.shape)}")
-    device = _one_device(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
-    s = _launch_stream(stream, device)
-    with torch.cuda.device(device), torch.cuda.stream(s):
+    here, handle = _launch_on(_one_device((q, k, positions, q_out, k_out), ("q", "k", "positions", "q_out", "k_out")), stream)
+    with here:
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k is not None and k_out is None:
@@ -747,8 +750,7 @@ def attn_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, 
         rc = lib().attn_rope(q.data_ptr(), q_out.data_ptr(), _rope_strides(q), _rope_strides(q_out), Hq,
                              k.data_ptr() if has_k else None, k_out.data_ptr() if has_k else None,
                              _rope_strides(k) if has_k else None, _rope_strides(k_out) if has_k else None,
-                             Hkv if has_k else 0, B, N, d, positions.data_ptr(), ctypes.byref(spec), int(bool(inverse)),
-                             s.cuda_stream)
+                             Hkv if has_k else 0, B, N, d, positions.data_ptr(), ctypes.byref(spec), int(bool(inverse)), handle)
     _check(rc, "attn_rope")
     return q_out, k_out
 
@@ -764,27 +766,33 @@ def kv_cache_fp8(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda"
     return pools[0], pools[1], scales.view(torch.float8_e8m0fnu)
 
 
-def _cache8_args(k_pool, v_pool, kv_scales, block_table, seq_lens, others):
-    """Types and shapes shared by the calls on the 8-bit cache, before any CUDA call.
-    ``others``: (tensor or None, name, dtype, dims) of the rest.  Returns
-    (S, num_pages, page_size, Hkv, d, max_pages)."""
-    for t, name, kind in ((k_pool, "k_pool", torch.float8_e4m3fn), (v_pool, "v_pool", torch.float8_e4m3fn),
-                          (kv_scales, "kv_scales", torch.float8_e8m0fnu)):
-        _require(t, name, torch.uint8 if isinstance(t, torch.Tensor) and t.dtype == torch.uint8 else kind, 4, cuda=False)
+_CACHE8 = ("k_pool", "v_pool", "kv_scales", "block_table", "seq_lens")
+_CACHE8_TYPES = (torch.float8_e4m3fn, torch.float8_e4m3fn, torch.float8_e8m0fnu)
+
+
+def _cache8_args(cache, more, names, types, dims):
+    """Types and shapes shared by the calls on the 8-bit cache, before any CUDA
+    call.  ``cache``: the tensors named in _CACHE8; ``more``: the call's others
+    (or None), with their names, types and numbers of dimensions.  Returns (S,
+    num_pages, page_size, Hkv, d, max_pages)."""
+    k_pool, v_pool, kv_scales, block_table, seq_lens = cache
+    for t, name, kind in zip(cache, _CACHE8, _CACHE8_TYPES):
+        _require(t, name, torch.uint8 if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 else kind, 4, cuda=False)
     _require(block_table, "block_table", torch.int32, 2, cuda=False)
     _require(seq_lens, "seq_lens", torch.int32, 1, cuda=False)
-    num_pages, page_size, Hkv, d = k_pool.shape
-    if v_pool.shape != k_pool.shape:
-        raise ValueError(f"v_pool shape {tuple(v_pool.shape)} differs from k_pool's {tuple(k_pool.shape)}")
-    if kv_scales.shape != (num_pages, Hkv, page_size, 2):
-        raise ValueError(f"kv_scales must be {(num_pages, Hkv, page_size, 2)}, got {tuple(kv_scales.shape)}")
-    S = seq_lens.shape[0]
-    if block_table.shape[0] != S:
-        raise ValueError(f"block_table {tuple(block_table.shape)} does not have one row per sequence ({S})")
-    for t, name, kind, nd in others:
+    for t, name, kind, nd in zip(more, names, types, dims):
         if t is not None:
             _require(t, name, kind, nd, cuda=False)
-    return S, num_pages, page_size, Hkv, d, block_table.shape[1]
+    shape = k_pool.shape
+    num_pages, page_size, Hkv, d = shape
+    if v_pool.shape != shape:
+        raise ValueError(f"v_pool shape {tuple(v_pool.shape)} differs from k_pool's {tuple(shape)}")
+    if kv_scales.shape != (num_pages, Hkv, page_size, 2):
+        raise ValueError(f"kv_scales must be {(num_pages, Hkv, page_size, 2)}, got {tuple(kv_scales.shape)}")
+    S, max_pages = block_table.shape
+    if seq_lens.shape[0] != S:
+        raise ValueError(f"block_table {tuple(block_table.shape)} does not have one row per sequence ({seq_lens.shape[0]})")
+    return S, num_pages, page_size, Hkv, d, max_pages
 
 
 def _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d):
@@ -802,19 +810,17 @@ def paged_kv_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.
     [num_pages,page_size,Hkv,d] float8_e4m3fn and kv_scales
     [num_pages,Hkv,page_size,2] float8_e8m0fnu (uint8 views of them are taken
     too), see kv_cache_fp8.  In place."""
+    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (k_new, v_new, cu_seqlens_q)
+    names = ("k_new", "v_new", "cu_seqlens_q")
     S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        k_pool, v_pool, kv_scales, block_table, seq_lens,
-        [(k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
-         (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)])
+        cache, more, names, (torch.bfloat16, torch.bfloat16, torch.int32), (3, 3, 1))
     _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
-    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens,
-                         k_new=k_new, v_new=v_new, cu_seqlens_q=cu_seqlens_q)
-    s = _launch_stream(stream, device)
-    with torch.cuda.device(device):
+    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
+    with here:
         rc = lib().paged_kv_append_fp8(k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                                        kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
                                        block_table.data_ptr(), S, k_new.shape[0], Hkv, d, page_size, max_pages, num_pages,
-                                       s.cuda_stream)
+                                       handle)
     _check(rc, "paged_kv_append_fp8")
 
 
@@ -828,28 +834,25 @@ def paged_rope_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Ten
     behind cu_seqlens_q[-1] are not written."""
     if not isinstance(spec, RopeSpec):
         raise TypeError("spec must come from rope_spec")
+    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (q, k_new, v_new, q_out, positions, cu_seqlens_q)
+    names = ("q", "k_new", "v_new", "q_out", "positions", "cu_seqlens_q")
     S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        k_pool, v_pool, kv_scales, block_table, seq_lens,
-        [(q, "q", torch.bfloat16, 3), (k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
-         (q_out, "q_out", torch.bfloat16, 3), (positions, "positions", torch.int32, 2),
-         (cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)])
+        cache, more, names, (torch.bfloat16,) * 4 + (torch.int32,) * 2, (3, 3, 3, 3, 2, 1))
     _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
     total_q, Hq = q.shape[:2]
     if q.shape != (k_new.shape[0], Hq, d) or (q_out is not None and q_out.shape != q.shape):
         raise ValueError("q / q_out do not match k_new")
     if positions.shape != (spec.num_axes, total_q):
         raise ValueError(f"positions must be {(spec.num_axes, total_q)}, got {tuple(positions.shape)}")
-    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, q=q,
-                         k_new=k_new, v_new=v_new, positions=positions, cu_seqlens_q=cu_seqlens_q, q_out=q_out)
-    s = _launch_stream(stream, device)
-    with torch.cuda.device(device), torch.cuda.stream(s):
+    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
+    with here:
         if q_out is None:
             q_out = torch.empty_like(q)
         rc = lib().paged_rope_append_fp8(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
                                          positions.data_ptr(), ctypes.byref(spec), k_pool.data_ptr(), v_pool.data_ptr(),
                                          kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
                                          block_table.data_ptr(), S, total_q, Hq, Hkv, d, page_size, max_pages, num_pages,
-                                         s.cuda_stream)
+                                         handle)
     _check(rc, "paged_rope_append_fp8")
     return q_out
 
@@ -861,10 +864,10 @@ def paged_kv_gather_fp8(k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: t
     goes to row cu_seqlens_k[s] + t of k_out / v_out [total_rows,Hkv,d].  Give
     the outputs, or ``total_rows`` to have them made (rows that no token falls
     on are then undefined).  Returns (k_out, v_out)."""
+    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (cu_seqlens_k, k_out, v_out)
+    names = ("cu_seqlens_k", "k_out", "v_out")
     S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        k_pool, v_pool, kv_scales, block_table, seq_lens,
-        [(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1), (k_out, "k_out", torch.bfloat16, 3),
-         (v_out, "v_out", torch.bfloat16, 3)])
+        cache, more, names, (torch.int32, torch.bfloat16, torch.bfloat16), (1, 3, 3))
     if cu_seqlens_k.shape[0] != S + 1:
         raise ValueError("cu_seqlens_k does not match the number of sequences")
     if (k_out is None) != (v_out is None):
@@ -878,16 +881,14 @@ def paged_kv_gather_fp8(k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: t
         raise ValueError("total_rows (or k_out and v_out) is needed")
     else:
         rows = int(total_rows)
-    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens,
-                         cu_seqlens_k=cu_seqlens_k, k_out=k_out, v_out=v_out)
-    s = _launch_stream(stream, device)
-    with torch.cuda.device(device), torch.cuda.stream(s):
+    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
+    with here:
         if k_out is None:
-            k_out = torch.empty((rows, Hkv, d), dtype=torch.bfloat16, device=device)
+            k_out = torch.empty((rows, Hkv, d), dtype=torch.bfloat16, device=k_pool.device)
             v_out = torch.empty_like(k_out)
         rc = lib().paged_kv_gather_fp8(k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
                                        seq_lens.data_ptr(), cu_seqlens_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), S,
-                                       rows, Hkv, d, page_size, max_pages, num_pages, s.cuda_stream)
+                                       rows, Hkv, d, page_size, max_pages, num_pages, handle)
     _check(rc, "paged_kv_gather_fp8")
     return k_out, v_out
 
@@ -904,9 +905,10 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
 
     q [S,Hq,d] bf16; block_table [S,max_pages] int32; seq_lens [S] int32, 0
     giving O = 0 and LSE = -inf.  Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32)."""
+    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (q, out, lse)
+    names = ("q", "out", "lse")
     S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        k_pool, v_pool, kv_scales, block_table, seq_lens,
-        [(q, "q", torch.bfloat16, 3), (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2)])
+        cache, more, names, (torch.bfloat16, torch.bfloat16, torch.float32), (3, 3, 2))
     Hq = q.shape[1]
     if q.shape != (S, Hq, d):
         raise ValueError(f"q must be [{S}, Hq, {d}], got {tuple(q.shape)}")
@@ -914,17 +916,15 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
         raise ValueError(f"out shape {tuple(out.shape)} differs from q's {tuple(q.shape)}")
     if lse is not None and lse.shape != (S, Hq):
         raise ValueError(f"lse shape {tuple(lse.shape)} is not ({S}, {Hq})")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if scale is None:
         scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
-    device = _one_device(k_pool=k_pool, v_pool=v_pool, kv_scales=kv_scales, block_table=block_table, seq_lens=seq_lens, q=q,
-                         out=out, lse=lse, workspace=workspace)
-    s = _launch_stream(stream, device)
-    with torch.cuda.device(device), torch.cuda.stream(s):
+    here, handle = _launch_on(_one_device(cache + more + (workspace,), _CACHE8 + names + ("workspace",)), stream)
+    with here:
         if workspace is None:
-            need = paged_attn_decode_fp8_workspace_bytes(S, Hq, Hkv, d, max_pages, page_size)
+            need = lib().paged_attn_decode_fp8_workspace_bytes(S, Hq, Hkv, d, max_pages, page_size)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        elif not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
@@ -932,6 +932,6 @@ def paged_attn_decode_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
         rc = lib().paged_attn_decode_fp8(
             q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), page_size, out.data_ptr(), lse.data_ptr(), S, Hq, Hkv, d, max_pages, num_pages,
-            float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s.cuda_stream)
+            float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
     _check(rc, "paged_attn_decode_fp8")
     return out, lse

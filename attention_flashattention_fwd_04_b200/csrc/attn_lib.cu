@@ -138,7 +138,8 @@ int append8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, 
 struct Decode8Plan {
   int hb = 0;    // KV heads of a tile
   int ctas = 0;  // CTAs of the split pass
-  size_t lse_offset = 0, tiles_offset = 0, total = 0;
+  int box = 0;   // tokens of one TMA box
+  size_t lse_offset = 0, total = 0;
 };
 
 bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size, Decode8Plan* out) {
@@ -149,20 +150,19 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   pl.hb = decode_heads_per_cta(Hkv);
   const int group = Hq / Hkv;
   const int tokens = attn::kDecode8Rows / pl.hb;
+  for (pl.box = 16; pl.box < tokens && page_size % (2 * pl.box) == 0;) pl.box *= 2;
   const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
   // Every CTA that the SMs hold at once (two an SM with up to 8 query heads a
   // KV head, one with 16), or one a tile.
   pl.ctas = static_cast<int>(std::min<long long>(tiles, group <= 8 ? 2 * 148 : 148));
   const size_t rows = 2 * static_cast<size_t>(pl.ctas) * pl.hb * group;
   pl.lse_offset = rows * d * sizeof(float);
-  pl.tiles_offset = pl.lse_offset + rows * sizeof(float);
-  pl.total = pl.tiles_offset + (attn::kDecode8MaxSeqs + 1) * sizeof(int32_t);
-  pl.total = (pl.total + 15) & ~static_cast<size_t>(15);
+  pl.total = (pl.lse_offset + rows * sizeof(float) + 15) & ~static_cast<size_t>(15);
   *out = pl;
   return true;
 }
 
-// 3-D map of bytes; inner rows of 128 or 64 bytes are swizzled, others not.
+// 3-D map of codes; rows of 128 or 64 bytes, swizzled as wide.
 bool encode_3d_bytes(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t stride1,
                      uint64_t stride2, uint32_t b0, uint32_t b1, uint32_t b2, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
@@ -177,25 +177,29 @@ bool encode_3d_bytes(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1
 }
 
 template <int D, int NT, int STAGES>
-int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& ts, const attn::Decode8Params& p,
-                   cudaStream_t stream) {
+int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Decode8Params& p, cudaStream_t stream) {
   using L = attn::Decode8Layout<D, STAGES>;
   auto kernel = attn::decode8_split_kernel<D, NT, STAGES>;
   cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, STAGES>>(L::kAlloc);
   if (e != cudaSuccess) return fail_cuda(e);
-  kernel<<<static_cast<unsigned>(p.ctas), attn::kDecode8Threads, L::kAlloc, stream>>>(tk, tv, ts, p);
+  kernel<<<static_cast<unsigned>(p.ctas), attn::kDecode8Threads, L::kAlloc, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail_cuda(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.Hq), static_cast<unsigned>(p.S));
-  cfg.blockDim = dim3(attn::kMerge8Threads);
+  // With few sequences and heads there are many partial rows for each: 16
+  // warps share a head's, else one warp takes them.
+  const bool wide = p.ctas > 16LL * p.S * (p.Hkv / p.hb);
+  const int heads = wide ? 1 : attn::kMerge8Warps;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.Hq + heads - 1) / heads), static_cast<unsigned>(p.S));
+  cfg.blockDim = dim3(32 * attn::kMerge8Warps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D>, p);
+  e = wide ? cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D, 16>, p)
+           : cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D, 1>, p);
   if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
@@ -318,23 +322,23 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
   if (st == ATTN_ERR_ALIGN || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse))
     return ATTN_ERR_ALIGN;
 
-  CUtensorMap tk, tv, ts;
+  CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(num_pages) * page_size;
   const uint64_t token_bytes = static_cast<uint64_t>(Hkv) * d;
   const uint32_t hb = static_cast<uint32_t>(pl.hb);
   const CUtensorMapSwizzle sw = d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  // Codes: (value, token row, head), a box the 16 tokens of HB heads; scales:
-  // (slot and K or V, head, page), the same tokens' 32 bytes a head.
-  if (!encode_3d_bytes(&tk, k_pool, d, rows, Hkv, token_bytes, d, d, 16, hb, sw) ||
-      !encode_3d_bytes(&tv, v_pool, d, rows, Hkv, token_bytes, d, d, 16, hb, sw) ||
-      !encode_3d_bytes(&ts, kv_scales, 2 * static_cast<uint64_t>(page_size), Hkv, num_pages, 2 * static_cast<uint64_t>(page_size),
-                       2 * static_cast<uint64_t>(page_size) * Hkv, 32, hb, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+  // (value, token row, head)
+  if (!encode_3d_bytes(&tk, k_pool, d, rows, Hkv, token_bytes, d, d, pl.box, hb, sw) ||
+      !encode_3d_bytes(&tv, v_pool, d, rows, Hkv, token_bytes, d, d, pl.box, hb, sw))
     return fail_cuda(cudaErrorInvalidValue);
 
   attn::Decode8Params p{};
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.lse_offset);
-  p.first_tile = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + pl.tiles_offset);
+  p.kv_scales = kv_scales;
+  p.box = pl.box;
+  const uint32_t page_chunks = static_cast<uint32_t>(page_size / 16);
+  p.page_inverse = page_chunks == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + page_chunks - 1) / page_chunks);
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.group = Hq / Hkv;
@@ -354,9 +358,9 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
     p.seq_lens = seq_lens + s0;
     int rc;
     if (d == 128)
-      rc = p.group <= 8 ? launch_decode8<128, 1, 3>(tk, tv, ts, p, s) : launch_decode8<128, 2, 6>(tk, tv, ts, p, s);
+      rc = p.group <= 8 ? launch_decode8<128, 1, 3>(tk, tv, p, s) : launch_decode8<128, 2, 6>(tk, tv, p, s);
     else
-      rc = p.group <= 8 ? launch_decode8<64, 1, 6>(tk, tv, ts, p, s) : launch_decode8<64, 2, 10>(tk, tv, ts, p, s);
+      rc = p.group <= 8 ? launch_decode8<64, 1, 6>(tk, tv, p, s) : launch_decode8<64, 2, 10>(tk, tv, p, s);
     if (rc != ATTN_OK) return rc;
   }
   return ATTN_OK;

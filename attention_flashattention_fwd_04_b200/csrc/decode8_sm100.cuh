@@ -44,19 +44,21 @@ struct Decode8Params {
   const int32_t* seq_lens;     // [S]
   __nv_bfloat16* o;            // [S, Hq, D]
   float* lse;                  // [S, Hq]
-  int32_t* first_tile;         // workspace [S + 1]: tiles before each sequence, of one group of heads
+  const uint8_t* kv_scales;    // [num_pages, Hkv, page_size, 2]
   float* part_lse;             // workspace [2 ctas, HB * group], in log2
   float* part_o;               // workspace [2 ctas, HB * group, D]
   int S, Hq, Hkv, group, page_size, max_pages, num_pages, hb, ctas;
+  int box;                     // tokens of one TMA box: 16 * 2^i, a divisor of page_size and of a tile's tokens
+  uint32_t page_inverse;       // ceil(2^32 / (page_size / 16)); 0 for page_size = 16
   float scale_log2;
 };
 
 template <int D, int STAGES>
 struct Decode8Layout {
   static constexpr int kPool = kDecode8Rows * D;          // codes of K (or V) of one tile
-  static constexpr int kScales = 1024;                    // 32 bytes a warp; a chunk's start on 128 bytes
-  static constexpr int kStage = 2 * kPool + kScales;
-  static constexpr int kBar = STAGES * kStage;
+  static constexpr int kStage = 2 * kPool;
+  static constexpr int kScales = STAGES * kStage;         // 32 bytes a warp and stage
+  static constexpr int kBar = kScales + STAGES * 32 * kDecode8Warps;
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
   static constexpr int kJoin = kWarpSums + kDecode8Warps * 4;  // the warps' bounds and sums, where they join
   static constexpr int kJoinBytes = 2 * kDecode8Warps * 16 * 4;
@@ -292,7 +294,7 @@ struct Decode8Warp {
 template <int D, int NT, int STAGES>
 __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_s, const Decode8Params p) {
+                         const Decode8Params p) {
   using L = Decode8Layout<D, STAGES>;
   // The merge may be launched once every CTA has begun; it waits for this grid.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -349,8 +351,6 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int s = threadIdx.x; s <= p.S; s += kDecode8Threads) p.first_tile[s] = first[s];
 
   const int groups = p.Hkv / p.hb;
   const long long total = static_cast<long long>(first[p.S]) * groups;
@@ -360,55 +360,73 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
 
   if (warp == kDecode8Warps) {
     // ------------------------------------------------------------ producer
-    const int chunks_per_tile = kDecode8Warps / p.hb;  // chunks of 16 tokens, one lane each
-    const uint32_t scale_stride = max(128, 32 * p.hb);
-    const uint32_t chunk_bytes = p.hb * 16 * (2 * D + 2);
+    const int chunks_per_tile = kDecode8Warps / p.hb;  // chunks of 16 tokens
+    const int chunks_per_box = p.box / 16, boxes_per_tile = chunks_per_tile / chunks_per_box;
+    const uint32_t box_bytes = p.hb * p.box * D;
+    // Scales go by cp.async, 16 bytes a lane (a tensor copy of so few bytes
+    // costs the copy engine as much as one of 16 KB): lanes 2 w and 2 w + 1
+    // bring those of consumer w.
+    const int w_hl = (lane >> 1) % p.hb, w_chunk = (lane >> 1) / p.hb;
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      tma_prefetch_desc(&tm_s);
     }
     bool ok = true;
-    int count = 0;  // tiles issued
+    int count = 0, st = 0;  // tiles issued, and the next one's place in the ring
+    uint32_t phase = 1;     // of the empty barriers: the ring's first round finds every place free
+    const int page_chunks = p.page_size / 16;
     for (long long at = begin; at < end && ok;) {
       const Decode8Run run = decode8_run(first, p.S, groups, at, end);
       at += run.to - run.from;
       const int len = p.seq_lens[run.s];
       const int chunk_end = min((len + 15) / 16, run.to * chunks_per_tile);
       const int32_t* table = p.block_table + static_cast<size_t>(run.s) * p.max_pages;
-      // Pages of 32 chunks at a time, one a lane; the next 32 are under way
-      // while these are used.
+      const int head = run.hg * p.hb;
+      // Where 32 chunks lie, one a lane (page << 4 | chunk of the page); the
+      // next 32 are under way while these are used.  The division by the
+      // page's chunks is a product with its inverse, exact below 2^28 chunks.
       int window = run.from * chunks_per_tile;
-      auto fetch = [&](int c) { return c < chunk_end ? table[c * 16 / p.page_size] : 0; };
-      int page = fetch(window + lane), next = fetch(window + 32 + lane);
-      for (int tile = run.from; tile < run.to; ++tile, ++count) {
+      auto fetch = [&](int c) -> uint32_t {
+        if (c >= chunk_end) return 0u;
+        const int i = p.page_inverse ? static_cast<int>(__umulhi(c, p.page_inverse)) : c;
+        const uint32_t page = static_cast<uint32_t>(table[i]);
+        if (page < static_cast<uint32_t>(p.num_pages)) return page << 4 | static_cast<uint32_t>(c - i * page_chunks);
+        atomicOr(&g_attn_device_error, kErrCache8Table);
+        return 0u;  // keeps every copy inside the pool; the result is flagged
+      };
+      uint32_t here = fetch(window + lane), next = fetch(window + 32 + lane);
+      for (int tile = run.from; tile < run.to; ++tile) {
         const int c0 = tile * chunks_per_tile;
         if (c0 >= window + 32) {
           window += 32;
-          page = next;
+          here = next;
           next = fetch(window + 32 + lane);
         }
-        int pg = __shfl_sync(0xffffffffu, page, (c0 - window + lane) & 31);
-        const int n = min(chunks_per_tile, chunk_end - c0);
-        const int st = count % STAGES, round = count / STAGES;
-        if (round > 0) ok = mbar_wait(empty_bar(st), (round - 1) & 1u, kErrCache8Wait);
+        const uint32_t of_scale = __shfl_sync(0xffffffffu, here, c0 - window + w_chunk);
+        const uint32_t of_box = __shfl_sync(0xffffffffu, here, c0 - window + lane * chunks_per_box);
+        const int n = min(chunks_per_tile, chunk_end - c0), boxes = chunks_per_box == 1 ? n : (n + chunks_per_box - 1) / chunks_per_box;
+        ok = mbar_wait(empty_bar(st), phase, kErrCache8Wait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), n * chunk_bytes);
-        __syncwarp();
-        if (lane < n) {
-          if (pg < 0 || pg >= p.num_pages) {
-            atomicOr(&g_attn_device_error, kErrCache8Table);
-            pg = 0;  // keeps every copy inside the pool; the result is flagged
-          }
-          const int slot = (c0 + lane) * 16 % p.page_size;
-          const uint32_t dst = base + st * L::kStage;
-          const int row = pg * p.page_size + slot, head = run.hg * p.hb;
-          tma_load_3d(dst + lane * p.hb * 16 * D, &tm_k, full_bar(st), 0, row, head);
-          tma_load_3d(dst + 2 * L::kPool + lane * scale_stride, &tm_s, full_bar(st), 2 * slot, head, pg);
-          tma_load_3d(dst + L::kPool + lane * p.hb * 16 * D, &tm_v, full_bar(st), 0, row, head);
+        if (lane < 16 && w_chunk < n) {
+          const size_t row = (static_cast<size_t>(of_scale >> 4) * p.Hkv + head + w_hl) * p.page_size + (of_scale & 15u) * 16;
+          cp_async_16(base + L::kScales + (st * 16 + lane) * 16, p.kv_scales + row * 2 + (lane & 1) * 16, 16);
         }
+        cp_async_mbar_arrive(full_bar(st));  // holds the phase open until the lane's copies have landed
         __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), 2 * boxes * box_bytes);
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t dst = base + st * L::kStage + lane * box_bytes;
+          const int row = static_cast<int>((of_box >> 4) * p.page_size + (of_box & 15u) * 16);
+          tma_load_3d(dst, &tm_k, full_bar(st), 0, row, head);
+          tma_load_3d(dst + L::kPool, &tm_v, full_bar(st), 0, row, head);
+        }
+        ++count;
+        if (++st == STAGES) {
+          st = 0;
+          phase ^= 1u;
+        }
       }
     }
     // No copy may be in flight when the CTA ends.
@@ -420,10 +438,12 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
   // -------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
   const int hl = warp % p.hb, chunk = warp / p.hb, parts = kDecode8Warps / p.hb;
-  const uint32_t scale_at = 2 * L::kPool + chunk * max(128, 32 * p.hb) + hl * 32;
+  const int chunks_per_box = p.box / 16;
+  const uint32_t rows_at = ((chunk / chunks_per_box * p.hb + hl) * chunks_per_box + chunk % chunks_per_box) * 16 * D;
   float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [2][warp][16 heads]
   float4* join_rows = reinterpret_cast<float4*>(smem + L::kJoinRows);  // [warp][lane]
-  int count = 0;
+  int st = 0;          // place in the ring, and phase of its full barriers
+  uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
   for (long long at = begin; at < end;) {
     const Decode8Run run = decode8_run(first, p.S, groups, at, end);
@@ -433,12 +453,11 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
     const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(hk) * p.group;
     Decode8Warp<D, NT> w;
     w.begin(p.q + head0 * D, p.group, p.scale_log2, grp, tig);
-    for (int tile = run.from; tile < run.to; ++tile, ++count) {
-      const int st = count % STAGES;
-      if (ok) ok = mbar_wait(full_bar(st), static_cast<uint32_t>(count / STAGES) & 1u, kErrCache8Wait);
+    for (int tile = run.from; tile < run.to; ++tile) {
+      if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
-      const uint32_t k = base + st * L::kStage + warp * 16 * D, v = k + L::kPool, sc = base + st * L::kStage + scale_at;
+      const uint32_t k = base + st * L::kStage + rows_at, v = k + L::kPool, sc = base + L::kScales + (st * 8 + warp) * 32;
       const int valid = len - tile * tokens - chunk * 16;
       if (valid >= 16)
         w.template tile<false>(k, v, sc, 16, lane);
@@ -446,6 +465,10 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
         w.template tile<true>(k, v, sc, valid, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(st));
+      if (++st == STAGES) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
     // Sums over the lanes that share a head.
 #pragma unroll
@@ -533,79 +556,149 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
   }
 }
 
-constexpr int kMerge8Threads = 128;
-
-// Joins the partial results of one sequence and query head, a CTA each:
+// Joins the partial results of the heads of a sequence:
 //     lse = log sum_i exp(lse_i),  O = sum_i exp(lse_i - lse) O_i.
-// Which CTAs hold them follows from first_tile as in the split pass; heads that
-// one CTA held alone are written already.  Each of the 4 warps adds up every
-// fourth partial row, and the four are added in their order.
-template <int D>
-__global__ void __launch_bounds__(kMerge8Threads) decode8_merge_kernel(const Decode8Params p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kWarps = kMerge8Threads / 32, kPer = D / 32;
-  __shared__ float rows[kWarps][D];
-  const int h = blockIdx.x, s = blockIdx.y;
+// Which CTAs of the split pass hold them follows from the lengths, summed up as
+// there; that part needs nothing of the split pass and runs before the wait for
+// it.  Heads that one CTA held alone are written already.  PER warps share a
+// head's partial rows, eight in flight at a time with their LSEs, so that the
+// join costs one trip to memory; the warps are added in their order.
+constexpr int kMerge8Warps = 16;
+
+template <int D, int PER>
+__global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const Decode8Params p) {
+  constexpr int kPer = D / 32, kHeads = kMerge8Warps / PER;
+  __shared__ float rows[PER > 1 ? kMerge8Warps : 1][D], bound[kMerge8Warps], sums[kMerge8Warps];
+  __shared__ int tiles[2][kMerge8Warps];
+  const int s = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int a0 = p.first_tile[s], n = p.first_tile[s + 1] - a0;
+  const int tokens = kDecode8Rows / p.hb, most = p.max_pages * p.page_size;
+  auto tiles_of = [&](int i) {
+    const int len = p.seq_lens[i];
+    return len < 0 || len > most ? 0 : (len + tokens - 1) / tokens;
+  };
+  int before = 0, all = 0;  // tiles of one group of heads: of the sequences before s, of all
+  for (int i = threadIdx.x; i < p.S; i += 32 * kMerge8Warps) {
+    const int x = tiles_of(i);
+    all += x;
+    if (i < s) before += x;
+  }
+  const int n = tiles_of(s);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+    all += __shfl_xor_sync(0xffffffffu, all, off);
+  }
+  if (lane == 0) {
+    tiles[0][warp] = before;
+    tiles[1][warp] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kMerge8Warps; ++w) {
+    before += tiles[0][w];
+    all += tiles[1][w];
+  }
+  const int h = blockIdx.x * kHeads + warp / PER, part = warp % PER;
+  const bool on = h < p.Hq;
   const size_t head = static_cast<size_t>(s) * p.Hq + h;
+  int pieces = 0;
+  size_t slot0 = 0;
+  const int hk = h / p.group, per_slot = p.hb * p.group, row0 = (hk % p.hb) * p.group + h % p.group;
+  if (n > 0) {
+    const int groups = p.Hkv / p.hb;
+    const long long total = static_cast<long long>(all) * groups;
+    const long long ctas = min(static_cast<long long>(p.ctas), total);
+    const long long at = static_cast<long long>(before) * groups + static_cast<long long>(hk / p.hb) * n;
+    // CTA c begins at tile c * total / ctas.
+    const int c0 = static_cast<int>(((at + 1) * ctas - 1) / total), c1 = static_cast<int>(((at + n) * ctas - 1) / total);
+    pieces = on ? c1 - c0 + 1 : 0;
+    slot0 = 2 * static_cast<size_t>(c0);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n == 0) {  // no tokens (or a length that the split pass reported)
-    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(p.o + head * D)[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) p.lse[head] = -INFINITY;
+    if (on && part == 0) {
+      if (lane < D / 8) reinterpret_cast<uint4*>(p.o + head * D)[lane] = make_uint4(0u, 0u, 0u, 0u);
+      if (lane == 0) p.lse[head] = -INFINITY;
+    }
     return;
   }
-  const int groups = p.Hkv / p.hb, hk = h / p.group;
-  const long long total = static_cast<long long>(p.first_tile[p.S]) * groups;
-  const long long ctas = min(static_cast<long long>(p.ctas), total);
-  const long long at = static_cast<long long>(a0) * groups + static_cast<long long>(hk / p.hb) * n;
-  // CTA c begins at tile c * total / ctas.
-  const int c0 = static_cast<int>(((at + 1) * ctas - 1) / total), c1 = static_cast<int>(((at + n) * ctas - 1) / total);
-  const int pieces = c1 - c0 + 1;
-  if (pieces == 1) return;
-  const int per_slot = p.hb * p.group, row0 = (hk % p.hb) * p.group + h % p.group;
-  auto row_of = [&](int i) { return static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * per_slot + row0; };
-  float mx = -INFINITY;
-  for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, p.part_lse[row_of(i)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float sum = 0.f;
-  for (int i = lane; i < pieces; i += 32) sum += ex2_approx(p.part_lse[row_of(i)] - mx);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  float out[kPer];
+  if (PER == 1 && pieces <= 1) return;
+  // The first piece ends its CTA (slot 1), the others begin theirs (slot 0).
+  auto row_of = [&](int i) { return (slot0 + 2 * i + (i == 0 ? 1 : 0)) * per_slot + row0; };
+  constexpr int kFlight = 8;
+  float mx = -INFINITY, sum = 0.f, out[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) out[e] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < pieces; i += kWarps) {
-    const size_t row = row_of(i);
-    const float w = ex2_approx(p.part_lse[row] - mx);
-    const float* src = p.part_o + row * D + lane * kPer;
-    if constexpr (kPer == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      out[0] = fmaf(w, x.x, out[0]);
-      out[1] = fmaf(w, x.y, out[1]);
-      out[2] = fmaf(w, x.z, out[2]);
-      out[3] = fmaf(w, x.w, out[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      out[0] = fmaf(w, x.x, out[0]);
-      out[1] = fmaf(w, x.y, out[1]);
+  if (pieces > 1) {
+    for (int i0 = part; i0 < pieces; i0 += PER * kFlight) {
+      float l[kFlight], x[kFlight][kPer];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * PER;
+        l[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[u][e] = 0.f;
+        if (i < pieces) {
+          const size_t row = row_of(i);
+          l[u] = p.part_lse[row];
+          const float* src = p.part_o + row * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src);
+            x[u][0] = y.x; x[u][1] = y.y; x[u][2] = y.z; x[u][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            x[u][0] = y.x; x[u][1] = y.y;
+          }
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) top = fmaxf(top, l[u]);
+      const float a = ex2_approx(mx - top);  // 0 the first time: there is a row, so top is above -inf (or all is NaN)
+      mx = top;
+      sum *= a;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) out[e] *= a;
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const float w = ex2_approx(l[u] - mx);
+        sum += w;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) out[e] = fmaf(w, x[u][e], out[e]);
+      }
     }
   }
+  if constexpr (PER > 1) {
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) rows[warp][lane * kPer + e] = out[e];
-  __syncthreads();
+    for (int e = 0; e < kPer; ++e) rows[warp][lane * kPer + e] = out[e];
+    if (lane == 0) {
+      bound[warp] = mx;
+      sums[warp] = sum;
+    }
+    __syncthreads();
+    if (part != 0 || pieces <= 1) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < PER; ++w) top = fmaxf(top, bound[warp + w]);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) out[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < PER; ++w) {
+      const float a = ex2_approx(bound[warp + w] - top);  // 0 for a warp without rows
+      sum = fmaf(a, sums[warp + w], sum);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) out[e] = fmaf(a, rows[warp + w][lane * kPer + e], out[e]);
+    }
+    mx = top;
+  }
   const float inv = 1.f / sum;
-  if (threadIdx.x < D / 2) {
-    float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      x += rows[w][2 * threadIdx.x];
-      y += rows[w][2 * threadIdx.x + 1];
-    }
-    reinterpret_cast<uint32_t*>(p.o + head * D)[threadIdx.x] = pack_bf16x2(x * inv, y * inv);
-  }
-  if (threadIdx.x == 0) p.lse[head] = (mx + log2f(sum)) * 0.69314718055994530942f;
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t*>(p.o + head * D + lane * kPer + e) = pack_bf16x2(out[e] * inv, out[e + 1] * inv);
+  if (lane == 0) p.lse[head] = (mx + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace attn
