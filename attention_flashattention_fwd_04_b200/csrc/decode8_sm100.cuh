@@ -10,9 +10,9 @@
 // tiles writes its output; others write partial results, at most two a CTA,
 // which decode8_merge_kernel joins.
 //
-// A producer warp brings tiles by TMA (codes and scales) into a ring; warp w of
-// the 8 consumers works on the tile's rows 16 w .. 16 w + 15, 16 tokens of one
-// head.  Both products run on mma.sync m16n8k16 with the cache as the 16-row
+// A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
+// each of the consumer warps works on 16 of the tile's rows, 16 tokens of one
+// KV head, for up to 8 or 16 of its query heads.  Both products run on mma.sync m16n8k16 with the cache as the 16-row
 // operand and the query heads of the group as the 8 columns (tcgen05's tiles
 // are far larger than a group of query heads, and there are a few FLOP per
 // byte): S^T = K Q^T and O^T += V^T P^T.
@@ -33,10 +33,9 @@
 
 namespace attn {
 
-constexpr int kDecode8Warps = 8;                           // consumers
-constexpr int kDecode8Threads = 32 * (kDecode8Warps + 1);  // and the producer
-constexpr int kDecode8Rows = 16 * kDecode8Warps;           // cached rows of a tile
-constexpr int kDecode8MaxSeqs = 1024;                      // sequences of one launch
+constexpr int kDecode8Parts = 8;                   // 16-row parts of a tile, a consumer warp each (or two)
+constexpr int kDecode8Rows = 16 * kDecode8Parts;   // cached rows of a tile
+constexpr int kDecode8MaxSeqs = 1024;              // sequences of one launch
 
 struct Decode8Params {
   const __nv_bfloat16* q;      // [S, Hq, D]
@@ -53,17 +52,18 @@ struct Decode8Params {
   float scale_log2;
 };
 
-template <int D, int STAGES>
+template <int D, int NW, int STAGES>
 struct Decode8Layout {
+  static constexpr int kWarps = kDecode8Parts * NW;       // consumers
+  static constexpr int kThreads = 32 * (kWarps + 1);      // and the producer
   static constexpr int kPool = kDecode8Rows * D;          // codes of K (or V) of one tile
   static constexpr int kStage = 2 * kPool;
   static constexpr int kScales = STAGES * kStage;         // 32 bytes a warp and stage
-  static constexpr int kBar = kScales + STAGES * 32 * kDecode8Warps;
+  static constexpr int kBar = kScales + STAGES * 32 * kDecode8Parts;
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
-  static constexpr int kJoin = kWarpSums + kDecode8Warps * 4;  // the warps' bounds and sums, where they join
-  static constexpr int kJoinBytes = 2 * kDecode8Warps * 16 * 4;
-  static constexpr int kJoinRows = kJoin + kJoinBytes;         // 16 bytes a lane
-  static constexpr int kTiles = kJoinRows + kDecode8Warps * 512;
+  static constexpr int kJoin = kWarpSums + kWarps * 4;     // bounds and sums of the warps, where they join
+  static constexpr int kJoinRows = kJoin + 2 * kWarps * 16 * 4;
+  static constexpr int kTiles = kJoinRows + kWarps * 1024;
   static constexpr int kBytes = kTiles + (kDecode8MaxSeqs + 1) * 4;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -121,9 +121,25 @@ __device__ __forceinline__ uint32_t decode8_offset(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+template <int THREADS>
 __device__ __forceinline__ void decode8_consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecode8Warps) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
+
+// Two 16 x 16 byte matrices (rows at the addresses of lanes 0-15 and 16-31),
+// transposed: a lane holds bytes of column lane / 4 (r0, r2) and lane / 4 + 8
+// (r1, r3), rows 4 (lane % 4) .. + 3.
+__device__ __forceinline__ void ldmatrix_b8_trans(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+// Token of the 16 in row r of the first product.  The second takes its tokens
+// in the order in which ldmatrix hands out bytes: lane tig has tokens 4 tig ..
+// + 3, as columns 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9.
+__device__ __forceinline__ int decode8_token(int r) { return 4 * ((r & 7) >> 1) + 2 * (r >> 3) + (r & 1); }
 
 // The tiles [from, to) of sequence s and head group hg, out of n.
 struct Decode8Run {
@@ -151,7 +167,7 @@ __device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, i
 // One tile for one warp.
 template <int D, int NT>
 struct Decode8Warp {
-  float acc[NT][D / 16][4];  // O^T: values 16 c + 2 grp (+ 1) of heads 2 tig (+ 1)
+  float acc[NT][D / 16][4];  // O^T: values 16 c + grp (0, 1) and + 8 (2, 3) of heads 2 tig (+ 1)
   float m[NT][2], l[NT][2];  // of heads 2 tig (+ 1); l is this lane's share
   float f[NT][2];            // scores' factor
   uint32_t q[NT][D / 16][2];
@@ -193,17 +209,17 @@ struct Decode8Warp {
     }
   }
 
-  // valid: the tokens of the 16 that belong to the sequence (TAIL: fewer than 16).
-  template <bool TAIL>
+  // valid: the tokens of the 16 that belong to the sequence.
   __device__ __forceinline__ void tile(uint32_t k, uint32_t v, uint32_t scales, int valid, int lane) {
     const int grp = lane >> 2, tig = lane & 3;
+    const int t0 = decode8_token(grp), t1 = t0 + 2;  // tokens of rows grp and grp + 8
     float sc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const int c = (D / 64) * tig + j;
-      const uint4 ka = lds_128(k + decode8_offset<D>(grp, c)), kb = lds_128(k + decode8_offset<D>(grp + 8, c));
+      const uint4 ka = lds_128(k + decode8_offset<D>(t0, c)), kb = lds_128(k + decode8_offset<D>(t1, c));
       const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -213,7 +229,17 @@ struct Decode8Warp {
         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt], a0, a1, a2, a3, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
       }
     }
-    const uint32_t e0 = lds_u16(scales + 2 * grp), e1 = lds_u16(scales + 2 * grp + 16);
+    if (valid < 16) {
+      // Tokens past the end may hold NaN codes, and 0 * NaN is NaN: their
+      // values are cleared (their scores below).
+      for (int i = lane; i < (16 - valid) * (D / 16); i += 32)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + decode8_offset<D>(valid + i / (D / 16), i % (D / 16))),
+                     "r"(0u)
+                     : "memory");
+      fence_proxy_async_smem();  // before the copies that will refill this place
+      __syncwarp();
+    }
+    const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
     const float k0 = cache8_scale(e0 & 255u), k1 = cache8_scale(e1 & 255u);
     const float v0 = static_cast<float>(static_cast<int>(e0 >> 8) - 127), v1 = static_cast<float>(static_cast<int>(e1 >> 8) - 127);
     bool up = false;
@@ -222,7 +248,7 @@ struct Decode8Warp {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool out = TAIL && grp + 8 * (e >> 1) >= valid;
+        const bool out = (e < 2 ? t0 : t1) >= valid;
         sc[nt][e] = out ? -INFINITY : sc[nt][e] * ((e < 2 ? k0 : k1) * f[nt][e & 1]);
         t[nt][e] = out ? -INFINITY : sc[nt][e] + (e < 2 ? v0 : v1);
         up |= t[nt][e] > m[nt][e & 1] + 8.f;
@@ -260,30 +286,14 @@ struct Decode8Warp {
       p[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
       p[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
     }
-    // Tokens past the end may hold NaN codes, and 0 * NaN is NaN: their codes
-    // are cleared (token 2 tig in the low half of a word, 2 tig + 1 in the high).
-    const uint32_t keep0 = (2 * tig < valid ? 0xffffu : 0u) | (2 * tig + 1 < valid ? 0xffff0000u : 0u);
-    const uint32_t keep1 = (2 * tig + 8 < valid ? 0xffffu : 0u) | (2 * tig + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
-      // Matrices: tokens 0-7 and 8-15 of vector c, then of vector c + 1.  Each
-      // 16-bit element is two codes (d, d + 1) of one token; transposed, a lane
-      // holds them for tokens 2 tig and 2 tig + 1, and bytes 1 and 2 change
-      // places so that each half is one d of both tokens.
-      uint32_t r[4];
-      const int row = (lane & 7) + (lane & 8), col = c + (lane >> 4);
-      ldmatrix_x4_trans(v + decode8_offset<D>(row, col), r[0], r[1], r[2], r[3]);
-      if (TAIL) {
-        r[0] &= keep0;
-        r[1] &= keep1;
-        r[2] &= keep0;
-        r[3] &= keep1;
-      }
+      uint32_t r[4];  // of vectors c (r[0], r[1]) and c + 1: 4 tokens' codes of values lane / 4 and lane / 4 + 8
+      ldmatrix_b8_trans(v + decode8_offset<D>(lane & 15, c + (lane >> 4)), r[0], r[1], r[2], r[3]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t x = __byte_perm(r[2 * u], 0u, 0x3120), y = __byte_perm(r[2 * u + 1], 0u, 0x3120);
-        const uint32_t a0 = e4m3x2_f16x2_lo(x), a1 = e4m3x2_f16x2_hi(x);
-        const uint32_t a2 = e4m3x2_f16x2_lo(y), a3 = e4m3x2_f16x2_hi(y);
+        const uint32_t a0 = e4m3x2_f16x2_lo(r[2 * u]), a1 = e4m3x2_f16x2_lo(r[2 * u + 1]);
+        const uint32_t a2 = e4m3x2_f16x2_hi(r[2 * u]), a3 = e4m3x2_f16x2_hi(r[2 * u + 1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][c + u], a0, a1, a2, a3, p[nt][0], p[nt][1]);
       }
@@ -291,11 +301,14 @@ struct Decode8Warp {
   }
 };
 
-template <int D, int NT, int STAGES>
-__global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
+// NT tiles of 8 query heads a warp, NW warps beside one another: up to
+// 8 NT NW query heads a KV head.
+template <int D, int NT, int NW, int STAGES>
+__global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 1 ? 2 : 1)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const Decode8Params p) {
-  using L = Decode8Layout<D, STAGES>;
+  using L = Decode8Layout<D, NW, STAGES>;
+  constexpr int kDecode8Warps = L::kWarps;
   // The merge may be launched once every CTA has begun; it waits for this grid.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
@@ -360,8 +373,8 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
 
   if (warp == kDecode8Warps) {
     // ------------------------------------------------------------ producer
-    const int chunks_per_tile = kDecode8Warps / p.hb;  // chunks of 16 tokens
-    const int chunks_per_box = p.box / 16, boxes_per_tile = chunks_per_tile / chunks_per_box;
+    const int chunks_per_tile = kDecode8Parts / p.hb;  // chunks of 16 tokens
+    const int chunks_per_box = p.box / 16;
     const uint32_t box_bytes = p.hb * p.box * D;
     // Scales go by cp.async, 16 bytes a lane (a tensor copy of so few bytes
     // costs the copy engine as much as one of 16 KB): lanes 2 w and 2 w + 1
@@ -408,9 +421,9 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
         ok = mbar_wait(empty_bar(st), phase, kErrCache8Wait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane < 16 && w_chunk < n) {
+        if (lane < 2 * kDecode8Parts && w_chunk < n) {
           const size_t row = (static_cast<size_t>(of_scale >> 4) * p.Hkv + head + w_hl) * p.page_size + (of_scale & 15u) * 16;
-          cp_async_16(base + L::kScales + (st * 16 + lane) * 16, p.kv_scales + row * 2 + (lane & 1) * 16, 16);
+          cp_async_16(base + L::kScales + (st * 2 * kDecode8Parts + lane) * 16, p.kv_scales + row * 2 + (lane & 1) * 16, 16);
         }
         cp_async_mbar_arrive(full_bar(st));  // holds the phase open until the lane's copies have landed
         __syncwarp();
@@ -437,11 +450,12 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
 
   // -------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
-  const int hl = warp % p.hb, chunk = warp / p.hb, parts = kDecode8Warps / p.hb;
+  const int part = warp % kDecode8Parts, q0 = warp / kDecode8Parts * 8 * NT;  // rows of the tile, and first query head
+  const int hl = part % p.hb, chunk = part / p.hb, parts = kDecode8Parts / p.hb;
   const int chunks_per_box = p.box / 16;
   const uint32_t rows_at = ((chunk / chunks_per_box * p.hb + hl) * chunks_per_box + chunk % chunks_per_box) * 16 * D;
-  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [2][warp][16 heads]
-  float4* join_rows = reinterpret_cast<float4*>(smem + L::kJoinRows);  // [warp][lane]
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);          // [2][warp][16 heads]
+  float* join_rows = reinterpret_cast<float*>(smem + L::kJoinRows);  // [warp][8][lane]
   int st = 0;          // place in the ring, and phase of its full barriers
   uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
@@ -450,19 +464,17 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
     at += run.to - run.from;
     const int len = p.seq_lens[run.s];
     const int hk = run.hg * p.hb + hl;
-    const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(hk) * p.group;
+    const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(hk) * p.group + q0;
+    const int mine = p.group - q0;  // query heads of this warp (8 NT at most)
     Decode8Warp<D, NT> w;
-    w.begin(p.q + head0 * D, p.group, p.scale_log2, grp, tig);
+    w.begin(p.q + head0 * D, mine, p.scale_log2, grp, tig);
     for (int tile = run.from; tile < run.to; ++tile) {
       if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
-      const uint32_t k = base + st * L::kStage + rows_at, v = k + L::kPool, sc = base + L::kScales + (st * 8 + warp) * 32;
+      const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + part) * 32;
       const int valid = len - tile * tokens - chunk * 16;
-      if (valid >= 16)
-        w.template tile<false>(k, v, sc, 16, lane);
-      else if (valid > 0)
-        w.template tile<true>(k, v, sc, valid, lane);
+      if (valid > 0) w.tile(k, k + L::kPool, sc, valid, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(st));
       if (++st == STAGES) {
@@ -485,15 +497,15 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             join[warp * 16 + nt * 8 + 2 * tig + u] = w.m[nt][u];
-            join[kDecode8Warps * 16 + warp * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
+            join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
           }
       }
-      decode8_consumers_sync();
+      decode8_consumers_sync<32 * kDecode8Warps>();
     }
     // Bound and sum of the head over its warps, and this warp's share of O.
     const bool whole = run.from == 0 && run.to == run.n;
-    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0);
-    const int rows = p.hb * p.group;
+    const size_t row0 = (2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0)) * p.hb * p.group + hl * p.group + q0;
+    const int warp0 = warp - chunk * p.hb;  // the head's first warp; the others follow at steps of hb
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -502,10 +514,10 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
         float mx = w.m[nt][u], sum = w.l[nt][u];
         if (parts > 1) {  // (the barriers of the rows' join below keep the next run from overwriting these)
           mx = -INFINITY;
-          for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[(i * p.hb + hl) * 16 + h]);
+          for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[(warp0 + i * p.hb) * 16 + h]);
           sum = 0.f;
           for (int i = 0; i < parts; ++i)
-            sum += join[kDecode8Warps * 16 + (i * p.hb + hl) * 16 + h] * ex2_approx(join[(i * p.hb + hl) * 16 + h] - mx);
+            sum += join[(kDecode8Warps + warp0 + i * p.hb) * 16 + h] * ex2_approx(join[(warp0 + i * p.hb) * 16 + h] - mx);
         }
         // O = acc * 2^(m - mx - 6) / sum
         const float a = ex2_approx(w.m[nt][u] - mx - 6.f) / sum;
@@ -514,44 +526,51 @@ __global__ void __launch_bounds__(kDecode8Threads, NT == 1 ? 2 : 1)
           w.acc[nt][c][u] *= a;
           w.acc[nt][c][u + 2] *= a;
         }
-        if (chunk == 0 && grp == 0 && h < p.group) {
+        if (chunk == 0 && grp == 0 && h < mine) {
           const float lse2 = mx + log2f(sum);
           if (whole)
             p.lse[head0 + h] = lse2 * 0.69314718055994530942f;
           else
-            p.part_lse[slot * rows + hl * p.group + h] = lse2;
+            p.part_lse[row0 + h] = lse2;
         }
       }
+    auto put = [&](size_t head, size_t row, int d, float x) {
+      if (whole)
+        p.o[head * D + d] = __float2bfloat16_rn(x);
+      else
+        p.part_o[row * D + d] = x;
+    };
+    if (parts == 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = nt * 8 + 2 * tig + (e & 1);
+          if (h >= mine) continue;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) put(head0 + h, row0 + h, 16 * c + grp + 8 * (e >> 1), w.acc[nt][c][e]);
+        }
+      continue;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        if (parts > 1) {
-          // The head's first warp adds up the others', in their order.
-          join_rows[threadIdx.x] = make_float4(w.acc[nt][c][0], w.acc[nt][c][1], w.acc[nt][c][2], w.acc[nt][c][3]);
-          decode8_consumers_sync();
-          if (chunk == 0) {
-            for (int i = 1; i < parts; ++i) {
-              const float4 x = join_rows[(i * p.hb + hl) * 32 + lane];
-              w.acc[nt][c][0] += x.x;
-              w.acc[nt][c][1] += x.y;
-              w.acc[nt][c][2] += x.z;
-              w.acc[nt][c][3] += x.w;
-            }
-          }
-          decode8_consumers_sync();
-        }
-        const int d = 16 * c + 2 * grp;
+      for (int c = 0; c < D / 16; c += 2) {
+        // 8 values a lane at a time go to shared memory; each thread adds up
+        // one of them over the head's warps, in their order, for each of the
+        // tile's heads.
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int h = nt * 8 + 2 * tig + u;
-          if (chunk != 0 || h >= p.group) continue;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(p.o + (head0 + h) * D + d) = pack_bf16x2(w.acc[nt][c][u], w.acc[nt][c][u + 2]);
-          else
-            *reinterpret_cast<float2*>(p.part_o + (slot * rows + hl * p.group + h) * D + d) =
-                make_float2(w.acc[nt][c][u], w.acc[nt][c][u + 2]);
+        for (int i = 0; i < 8; ++i) join_rows[(warp * 8 + i) * 32 + lane] = w.acc[nt][c + i / 4][i % 4];
+        decode8_consumers_sync<32 * kDecode8Warps>();
+        const int i = part, h = nt * 8 + 2 * tig + (i & 1), d = 16 * (c + i / 4) + grp + 8 * ((i >> 1) & 1);
+        if (h < mine) {
+          for (int g = 0; g < p.hb; ++g) {
+            float x = 0.f;
+            for (int j = 0; j < parts; ++j) x += join_rows[((warp - part + j * p.hb + g) * 8 + i) * 32 + lane];
+            put(head0 + (g - hl) * p.group + h, row0 + (g - hl) * p.group + h, d, x);
+          }
         }
+        decode8_consumers_sync<32 * kDecode8Warps>();
       }
   }
 }
