@@ -152,6 +152,7 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   const int tokens = attn::kDecode8Rows / pl.hb;
   for (pl.box = 16; pl.box < tokens && page_size % (2 * pl.box) == 0;) pl.box *= 2;
   const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
+  if (tiles > INT_MAX) return false;
   // Every CTA that the SMs hold at once (see paged_attn_decode_fp8), or one a tile.
   pl.ctas = static_cast<int>(std::min<long long>(tiles, d == 64 || group <= 8 ? 2 * 148 : 148));
   const size_t rows = 2 * static_cast<size_t>(pl.ctas) * pl.hb * group;
@@ -175,11 +176,11 @@ bool encode_3d_bytes(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT, int NW, int STAGES>
+template <int D, int NT, int PER_SM, int STAGES>
 int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Decode8Params& p, cudaStream_t stream) {
-  using L = attn::Decode8Layout<D, NW, STAGES>;
-  auto kernel = attn::decode8_split_kernel<D, NT, NW, STAGES>;
-  cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, NW, STAGES>>(L::kAlloc);
+  using L = attn::Decode8Layout<D, STAGES>;
+  auto kernel = attn::decode8_split_kernel<D, NT, PER_SM, STAGES>;
+  cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, PER_SM, STAGES>>(L::kAlloc);
   if (e != cudaSuccess) return fail_cuda(e);
   kernel<<<static_cast<unsigned>(p.ctas), L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
   e = cudaGetLastError();
@@ -345,6 +346,7 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.hb = pl.hb;
+  for (p.hb_log2 = 0; 1 << p.hb_log2 < pl.hb;) ++p.hb_log2;
   p.ctas = pl.ctas;
   p.scale_log2 = scale * kLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -355,14 +357,12 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
     p.lse = lse + static_cast<size_t>(s0) * Hq;
     p.block_table = block_table + static_cast<size_t>(s0) * max_pages;
     p.seq_lens = seq_lens + s0;
-    // Two CTAs an SM, with 9 to 16 query heads a KV head one warp for all of
-    // them at d = 64; at d = 128 that does not fit the registers: two warps,
-    // 8 heads each, and one CTA an SM.
+    // Two CTAs an SM, but one where 16 query heads of d = 128 need its registers.
     int rc;
     if (d == 128)
-      rc = p.group <= 8 ? launch_decode8<128, 1, 1, 3>(tk, tv, p, s) : launch_decode8<128, 1, 2, 6>(tk, tv, p, s);
+      rc = p.group <= 8 ? launch_decode8<128, 1, 2, 3>(tk, tv, p, s) : launch_decode8<128, 2, 1, 6>(tk, tv, p, s);
     else
-      rc = p.group <= 8 ? launch_decode8<64, 1, 1, 6>(tk, tv, p, s) : launch_decode8<64, 2, 1, 6>(tk, tv, p, s);
+      rc = p.group <= 8 ? launch_decode8<64, 1, 2, 6>(tk, tv, p, s) : launch_decode8<64, 2, 2, 6>(tk, tv, p, s);
     if (rc != ATTN_OK) return rc;
   }
   return ATTN_OK;

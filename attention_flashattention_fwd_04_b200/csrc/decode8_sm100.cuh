@@ -11,10 +11,10 @@
 // which decode8_merge_kernel joins.
 //
 // A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
-// each of the consumer warps works on 16 of the tile's rows, 16 tokens of one
-// KV head, for up to 8 or 16 of its query heads.  Both products run on mma.sync m16n8k16 with the cache as the 16-row
-// operand and the query heads of the group as the 8 columns (tcgen05's tiles
-// are far larger than a group of query heads, and there are a few FLOP per
+// each of the 8 consumer warps works on 16 of the tile's rows, 16 tokens of one
+// KV head, for 8 NT of its query heads.  Both products run on mma.sync m16n8k16
+// with the cache as the 16-row operand and the query heads as columns (tcgen05's
+// tiles are far larger than a group of query heads, and there are a few FLOP per
 // byte): S^T = K Q^T and O^T += V^T P^T.
 //   - e4m3 codes become f16 exactly; q, scaled by a power of two of its row to
 //     use f16's range, keeps its 8 bits (values 2^-28 below the row's largest
@@ -33,8 +33,10 @@
 
 namespace attn {
 
-constexpr int kDecode8Parts = 8;                   // 16-row parts of a tile, a consumer warp each (or two)
+constexpr int kDecode8Parts = 8;                   // 16-row parts of a tile, a consumer warp each
+constexpr int kDecode8RowsLog2 = 7;
 constexpr int kDecode8Rows = 16 * kDecode8Parts;   // cached rows of a tile
+static_assert(kDecode8Rows == 1 << kDecode8RowsLog2, "a tile is 8 warps of 16 rows");
 constexpr int kDecode8MaxSeqs = 1024;              // sequences of one launch
 
 struct Decode8Params {
@@ -46,24 +48,23 @@ struct Decode8Params {
   const uint8_t* kv_scales;    // [num_pages, Hkv, page_size, 2]
   float* part_lse;             // workspace [2 ctas, HB * group], in log2
   float* part_o;               // workspace [2 ctas, HB * group, D]
-  int S, Hq, Hkv, group, page_size, max_pages, num_pages, hb, ctas;
+  int S, Hq, Hkv, group, page_size, max_pages, num_pages, hb, hb_log2, ctas;
   int box;                     // tokens of one TMA box: 16 * 2^i, a divisor of page_size and of a tile's tokens
   uint32_t page_inverse;       // ceil(2^32 / (page_size / 16)); 0 for page_size = 16
   float scale_log2;
 };
 
-template <int D, int NW, int STAGES>
+template <int D, int STAGES>
 struct Decode8Layout {
-  static constexpr int kWarps = kDecode8Parts * NW;       // consumers
+  static constexpr int kWarps = kDecode8Parts;            // consumers
   static constexpr int kThreads = 32 * (kWarps + 1);      // and the producer
   static constexpr int kPool = kDecode8Rows * D;          // codes of K (or V) of one tile
   static constexpr int kStage = 2 * kPool;
   static constexpr int kScales = STAGES * kStage;         // 32 bytes a warp and stage
   static constexpr int kBar = kScales + STAGES * 32 * kDecode8Parts;
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
-  static constexpr int kJoin = kWarpSums + kWarps * 4;     // bounds and sums of the warps, where they join
-  static constexpr int kJoinRows = kJoin + 2 * kWarps * 16 * 4;
-  static constexpr int kTiles = kJoinRows + kWarps * 1024;
+  static constexpr int kJoin = kWarpSums + kWarps * 4;    // bounds and sums of the warps, [2][warp][16 heads]
+  static constexpr int kTiles = kJoin + 2 * kWarps * 16 * 4;
   static constexpr int kBytes = kTiles + (kDecode8MaxSeqs + 1) * 4;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -141,26 +142,41 @@ __device__ __forceinline__ void ldmatrix_b8_trans(uint32_t addr, uint32_t& r0, u
 // + 3, as columns 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9.
 __device__ __forceinline__ int decode8_token(int r) { return 4 * ((r & 7) >> 1) + 2 * (r >> 3) + (r & 1); }
 
+// CTA c of n takes total / n tiles, and one more if c < total % n.
+struct Decode8Share {
+  int each, more;
+  __device__ __forceinline__ Decode8Share(int total, int n) : each(total / n), more(total % n) {}
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int cut = more * (each + 1);
+    return tile < cut ? tile / (each + 1) : more + (tile - cut) / each;
+  }
+};
+
 // The tiles [from, to) of sequence s and head group hg, out of n.
 struct Decode8Run {
   int s, hg, from, to, n;
 };
 
-// The run that begins at tile `at` of all, cut at `end`.  first: first_tile in
-// shared memory.
-__device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, int groups, long long at, long long end) {
+// The run that begins at tile `at` of all, cut at `end`.  first: the tiles of one
+// head group before each sequence.
+__device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, int groups, int at, int end) {
   int lo = 0, hi = S;  // the last sequence that begins at or before tile `at`: it is not empty, since at < total
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (static_cast<long long>(first[mid]) * groups <= at) lo = mid; else hi = mid;
+    if (first[mid] * groups <= at) lo = mid; else hi = mid;
   }
   Decode8Run r;
   r.s = lo;
-  r.n = first[lo + 1] - first[lo];
-  const long long in = at - static_cast<long long>(first[lo]) * groups;
-  r.hg = static_cast<int>(in / r.n);
-  r.from = static_cast<int>(in % r.n);
-  r.to = static_cast<int>(min(static_cast<long long>(r.n), r.from + (end - at)));
+  const int before = first[lo];
+  r.n = first[lo + 1] - before;
+  r.from = at - before * groups;
+  r.hg = 0;
+  if (groups > 1) {
+    r.hg = r.from / r.n;
+    r.from -= r.hg * r.n;
+  }
+  r.to = min(r.n, r.from + (end - at));
   return r;
 }
 
@@ -241,7 +257,8 @@ struct Decode8Warp {
     }
     const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
     const float k0 = cache8_scale(e0 & 255u), k1 = cache8_scale(e1 & 255u);
-    const float v0 = static_cast<float>(static_cast<int>(e0 >> 8) - 127), v1 = static_cast<float>(static_cast<int>(e1 >> 8) - 127);
+    // The exponents of V as floats: a byte in the last bits of 2^23.
+    float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388735.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388735.f;
     bool up = false;
     float t[NT][4];
 #pragma unroll
@@ -301,13 +318,12 @@ struct Decode8Warp {
   }
 };
 
-// NT tiles of 8 query heads a warp, NW warps beside one another: up to
-// 8 NT NW query heads a KV head.
-template <int D, int NT, int NW, int STAGES>
-__global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 1 ? 2 : 1)
+// NT tiles of 8 query heads a KV head.  PER_SM: CTAs an SM.
+template <int D, int NT, int PER_SM, int STAGES>
+__global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const Decode8Params p) {
-  using L = Decode8Layout<D, NW, STAGES>;
+  using L = Decode8Layout<D, STAGES>;
   constexpr int kDecode8Warps = L::kWarps;
   // The merge may be launched once every CTA has begun; it waits for this grid.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
   int32_t* first = reinterpret_cast<int32_t*>(smem + L::kTiles);
   int32_t* warp_sums = reinterpret_cast<int32_t*>(smem + L::kWarpSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tokens = kDecode8Rows / p.hb;  // of a tile
+  const int tokens_log2 = kDecode8RowsLog2 - p.hb_log2, tokens = 1 << tokens_log2;  // of a tile
 
   // Tiles before each sequence: every consumer thread sums up a run of
   // lengths, the warps' sums follow.
@@ -335,7 +351,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
         if (blockIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
         len = 0;
       }
-      own += (len + tokens - 1) / tokens;
+      own += (len + tokens - 1) >> tokens_log2;
       first[s + 1] = own;
     }
     before = own;
@@ -365,21 +381,22 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
   }
   __syncthreads();
 
-  const int groups = p.Hkv / p.hb;
-  const long long total = static_cast<long long>(first[p.S]) * groups;
-  const long long ctas = min(static_cast<long long>(p.ctas), total);
-  if (static_cast<long long>(blockIdx.x) >= ctas) return;
-  const long long begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
+  const int groups = p.Hkv >> p.hb_log2;
+  const int total = first[p.S] * groups;
+  const int ctas = min(p.ctas, total);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const Decode8Share share(total, ctas);
+  const int begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
 
   if (warp == kDecode8Warps) {
     // ------------------------------------------------------------ producer
-    const int chunks_per_tile = kDecode8Parts / p.hb;  // chunks of 16 tokens
+    const int chunks_per_tile = kDecode8Parts >> p.hb_log2;  // chunks of 16 tokens
     const int chunks_per_box = p.box / 16;
     const uint32_t box_bytes = p.hb * p.box * D;
     // Scales go by cp.async, 16 bytes a lane (a tensor copy of so few bytes
     // costs the copy engine as much as one of 16 KB): lanes 2 w and 2 w + 1
     // bring those of consumer w.
-    const int w_hl = (lane >> 1) % p.hb, w_chunk = (lane >> 1) / p.hb;
+    const int w_hl = (lane >> 1) & (p.hb - 1), w_chunk = lane >> (1 + p.hb_log2);
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
     int count = 0, st = 0;  // tiles issued, and the next one's place in the ring
     uint32_t phase = 1;     // of the empty barriers: the ring's first round finds every place free
     const int page_chunks = p.page_size / 16;
-    for (long long at = begin; at < end && ok;) {
+    for (int at = begin; at < end && ok;) {
       const Decode8Run run = decode8_run(first, p.S, groups, at, end);
       at += run.to - run.from;
       const int len = p.seq_lens[run.s];
@@ -441,6 +458,17 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
           phase ^= 1u;
         }
       }
+      // The consumers write the run's result through NT places of the ring.
+      for (int i = 0; i < NT && ok; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(st), phase, kErrCache8Wait));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(full_bar(st));
+        ++count;
+        if (++st == STAGES) {
+          st = 0;
+          phase ^= 1u;
+        }
+      }
     }
     // No copy may be in flight when the CTA ends.
     for (int c = max(0, count - STAGES); c < count; ++c)
@@ -450,29 +478,24 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
 
   // -------------------------------------------------------------- consumers
   const int grp = lane >> 2, tig = lane & 3;
-  const int part = warp % kDecode8Parts, q0 = warp / kDecode8Parts * 8 * NT;  // rows of the tile, and first query head
-  const int hl = part % p.hb, chunk = part / p.hb, parts = kDecode8Parts / p.hb;
+  const int hl = warp & (p.hb - 1), chunk = warp >> p.hb_log2, parts = kDecode8Parts >> p.hb_log2;
   const int chunks_per_box = p.box / 16;
   const uint32_t rows_at = ((chunk / chunks_per_box * p.hb + hl) * chunks_per_box + chunk % chunks_per_box) * 16 * D;
-  float* join = reinterpret_cast<float*>(smem + L::kJoin);          // [2][warp][16 heads]
-  float* join_rows = reinterpret_cast<float*>(smem + L::kJoinRows);  // [warp][8][lane]
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [2][warp][16 heads]: bounds, later factors; sums
   int st = 0;          // place in the ring, and phase of its full barriers
   uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
-  for (long long at = begin; at < end;) {
+  for (int at = begin; at < end;) {
     const Decode8Run run = decode8_run(first, p.S, groups, at, end);
     at += run.to - run.from;
     const int len = p.seq_lens[run.s];
-    const int hk = run.hg * p.hb + hl;
-    const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(hk) * p.group + q0;
-    const int mine = p.group - q0;  // query heads of this warp (8 NT at most)
     Decode8Warp<D, NT> w;
-    w.begin(p.q + head0 * D, mine, p.scale_log2, grp, tig);
+    w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_log2, grp, tig);
     for (int tile = run.from; tile < run.to; ++tile) {
       if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) continue;
-      const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + part) * 32;
+      const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + warp) * 32;
       const int valid = len - tile * tokens - chunk * 16;
       if (valid > 0) w.tile(k, k + L::kPool, sc, valid, lane);
       __syncwarp();
@@ -482,96 +505,92 @@ __global__ void __launch_bounds__(Decode8Layout<D, NW, STAGES>::kThreads, NW == 
         phase ^= 1u;
       }
     }
-    // Sums over the lanes that share a head.
+    // The run's result.  Bounds, sums and O^T go to shared memory (O^T to the
+    // ring's next NT places), one thread a head works out what each of the
+    // head's warps counts, and all threads add up and write O, 8 values at a
+    // time.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) w.l[nt][u] += __shfl_xor_sync(0xffffffffu, w.l[nt][u], off);
-    if (parts > 1) {
-      // The warps of one head hold different tokens.
-      if (grp == 0) {
+    uint32_t place[NT];
+    decode8_consumers_sync<32 * kDecode8Warps>();  // the last run's factors have been read
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            join[warp * 16 + nt * 8 + 2 * tig + u] = w.m[nt][u];
-            join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
-          }
+    for (int nt = 0; nt < NT; ++nt) {
+      if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
+      place[nt] = st;
+      if (++st == STAGES) {
+        st = 0;
+        phase ^= 1u;
       }
-      decode8_consumers_sync<32 * kDecode8Warps>();
-    }
-    // Bound and sum of the head over its warps, and this warp's share of O.
-    const bool whole = run.from == 0 && run.to == run.n;
-    const size_t row0 = (2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0)) * p.hb * p.group + hl * p.group + q0;
-    const int warp0 = warp - chunk * p.hb;  // the head's first warp; the others follow at steps of hb
+      float* out = reinterpret_cast<float*>(smem + place[nt] * L::kStage) + warp * (D / 4) * 32;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = nt * 8 + 2 * tig + u;
-        float mx = w.m[nt][u], sum = w.l[nt][u];
-        if (parts > 1) {  // (the barriers of the rows' join below keep the next run from overwriting these)
-          mx = -INFINITY;
-          for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[(warp0 + i * p.hb) * 16 + h]);
-          sum = 0.f;
-          for (int i = 0; i < parts; ++i)
-            sum += join[(kDecode8Warps + warp0 + i * p.hb) * 16 + h] * ex2_approx(join[(warp0 + i * p.hb) * 16 + h] - mx);
-        }
-        // O = acc * 2^(m - mx - 6) / sum
-        const float a = ex2_approx(w.m[nt][u] - mx - 6.f) / sum;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          w.acc[nt][c][u] *= a;
-          w.acc[nt][c][u + 2] *= a;
-        }
-        if (chunk == 0 && grp == 0 && h < mine) {
-          const float lse2 = mx + log2f(sum);
-          if (whole)
-            p.lse[head0 + h] = lse2 * 0.69314718055994530942f;
-          else
-            p.part_lse[row0 + h] = lse2;
-        }
-      }
-    auto put = [&](size_t head, size_t row, int d, float x) {
-      if (whole)
-        p.o[head * D + d] = __float2bfloat16_rn(x);
-      else
-        p.part_o[row * D + d] = x;
-    };
-    if (parts == 1) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int c = 0; c < D / 16; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int h = nt * 8 + 2 * tig + (e & 1);
-          if (h >= mine) continue;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) put(head0 + h, row0 + h, 16 * c + grp + 8 * (e >> 1), w.acc[nt][c][e]);
+          const int k = 4 * c + e;  // rows of 32 lanes; lane ^ k keeps the readers below off one bank
+          out[k * 32 + (lane ^ k)] = w.acc[nt][c][e];
         }
-      continue;
-    }
+      if (grp == 0) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < D / 16; c += 2) {
-        // 8 values a lane at a time go to shared memory; each thread adds up
-        // one of them over the head's warps, in their order, for each of the
-        // tile's heads.
-#pragma unroll
-        for (int i = 0; i < 8; ++i) join_rows[(warp * 8 + i) * 32 + lane] = w.acc[nt][c + i / 4][i % 4];
-        decode8_consumers_sync<32 * kDecode8Warps>();
-        const int i = part, h = nt * 8 + 2 * tig + (i & 1), d = 16 * (c + i / 4) + grp + 8 * ((i >> 1) & 1);
-        if (h < mine) {
-          for (int g = 0; g < p.hb; ++g) {
-            float x = 0.f;
-            for (int j = 0; j < parts; ++j) x += join_rows[((warp - part + j * p.hb + g) * 8 + i) * 32 + lane];
-            put(head0 + (g - hl) * p.group + h, row0 + (g - hl) * p.group + h, d, x);
-          }
+        for (int u = 0; u < 2; ++u) {
+          join[warp * 16 + nt * 8 + 2 * tig + u] = w.m[nt][u];
+          join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
         }
-        decode8_consumers_sync<32 * kDecode8Warps>();
       }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    decode8_consumers_sync<32 * kDecode8Warps>();
+    const bool whole = run.from == 0 && run.to == run.n;
+    const size_t row0 = (2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0)) * p.hb * p.group;
+    const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(run.hg) * p.hb * p.group;
+    const int heads = p.hb * p.group;  // rows of the result
+    if (static_cast<int>(threadIdx.x) < heads) {
+      const int g = threadIdx.x / p.group, at_head = g * 16 + threadIdx.x % p.group;
+      float mx = -INFINITY, sum = 0.f;
+      for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[i * p.hb * 16 + at_head]);
+      for (int i = 0; i < parts; ++i)
+        sum += join[(kDecode8Warps + i * p.hb) * 16 + at_head] * ex2_approx(join[i * p.hb * 16 + at_head] - mx);
+      // O = sum over the warps of acc * 2^(m - mx - 6) / sum
+      for (int i = 0; i < parts; ++i)
+        join[i * p.hb * 16 + at_head] = ex2_approx(join[i * p.hb * 16 + at_head] - mx - 6.f) / sum;
+      const float lse2 = mx + log2f(sum);
+      if (whole)
+        p.lse[head0 + threadIdx.x] = lse2 * 0.69314718055994530942f;
+      else
+        p.part_lse[row0 + threadIdx.x] = lse2;
+    }
+    decode8_consumers_sync<32 * kDecode8Warps>();
+    for (int i = threadIdx.x; i < heads * (D / 8); i += 32 * kDecode8Warps) {
+      const int row = i / (D / 8), octet = i % (D / 8);
+      const int g = row / p.group, h = row % p.group;
+      const int k = 2 * octet + (h & 1), t = (h & 7) >> 1;
+      const float* src = reinterpret_cast<const float*>(smem + (NT == 1 || h < 8 ? place[0] : place[NT - 1]) * L::kStage);
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = 0.f;
+      for (int part = 0; part < parts; ++part) {
+        const int from = part * p.hb + g;
+        const float a = join[from * 16 + h];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = fmaf(a, src[(from * (D / 4) + k) * 32 + ((4 * u + t) ^ k)], x[u]);
+      }
+      if (whole) {
+        *reinterpret_cast<uint4*>(p.o + (head0 + row) * D + 8 * octet) = pack_bf16x8(x);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (row0 + row) * D + 8 * octet);
+        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+      }
+    }
+    fence_proxy_async_smem();  // before the copies that will refill these places
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mbar_arrive(empty_bar(place[nt]));
+    }
   }
 }
 
@@ -591,10 +610,10 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
   __shared__ int tiles[2][kMerge8Warps];
   const int s = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tokens = kDecode8Rows / p.hb, most = p.max_pages * p.page_size;
+  const int tokens_log2 = kDecode8RowsLog2 - p.hb_log2, most = p.max_pages * p.page_size;
   auto tiles_of = [&](int i) {
     const int len = p.seq_lens[i];
-    return len < 0 || len > most ? 0 : (len + tokens - 1) / tokens;
+    return len < 0 || len > most ? 0 : (len + (1 << tokens_log2) - 1) >> tokens_log2;
   };
   int before = 0, all = 0;  // tiles of one group of heads: of the sequences before s, of all
   for (int i = threadIdx.x; i < p.S; i += 32 * kMerge8Warps) {
@@ -624,14 +643,12 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
   const size_t head = static_cast<size_t>(s) * p.Hq + h;
   int pieces = 0;
   size_t slot0 = 0;
-  const int hk = h / p.group, per_slot = p.hb * p.group, row0 = (hk % p.hb) * p.group + h % p.group;
+  const int hk = h / p.group, per_slot = p.hb * p.group, row0 = (hk & (p.hb - 1)) * p.group + h % p.group;
   if (n > 0) {
-    const int groups = p.Hkv / p.hb;
-    const long long total = static_cast<long long>(all) * groups;
-    const long long ctas = min(static_cast<long long>(p.ctas), total);
-    const long long at = static_cast<long long>(before) * groups + static_cast<long long>(hk / p.hb) * n;
-    // CTA c begins at tile c * total / ctas.
-    const int c0 = static_cast<int>(((at + 1) * ctas - 1) / total), c1 = static_cast<int>(((at + n) * ctas - 1) / total);
+    const int groups = p.Hkv >> p.hb_log2, total = all * groups;
+    const Decode8Share share(total, min(p.ctas, total));
+    const int at = before * groups + (hk >> p.hb_log2) * n;
+    const int c0 = share.owner(at), c1 = share.owner(at + n - 1);
     pieces = on ? c1 - c0 + 1 : 0;
     slot0 = 2 * static_cast<size_t>(c0);
   }

@@ -298,8 +298,17 @@ def test_decode_share_out(seed):
         total = int(first[-1]) * groups
         ctas = min(int(rng.integers(1, 60)), total)
         seen, slots = set(), {}
+        each, more = divmod(total, ctas) if ctas else (0, 0)
+
+        def begin(c):
+            return c * each + min(c, more)
+
+        def owner(t):
+            cut = more * (each + 1)
+            return t // (each + 1) if t < cut else more + (t - cut) // each
+
         for c in range(ctas):
-            at, end = c * total // ctas, (c + 1) * total // ctas
+            at, end = begin(c), begin(c + 1)
             assert at < end
             while at < end:
                 lo, hi = 0, S
@@ -324,7 +333,7 @@ def test_decode_share_out(seed):
             n = int(first[s + 1] - first[s])
             for hg in range(groups if n else 0):
                 at = int(first[s]) * groups + hg * n
-                c0, c1 = ((at + 1) * ctas - 1) // total, ((at + n) * ctas - 1) // total
+                c0, c1 = owner(at), owner(at + n - 1)
                 if c1 > c0:
                     read.update({2 * (c0 + i) + (1 if i == 0 else 0): (s, hg) for i in range(c1 - c0 + 1)})
         assert read == slots
