@@ -80,10 +80,19 @@ int validate_cache8(const void* k_pool, const void* v_pool, const void* kv_scale
   return ATTN_OK;
 }
 
+// Blocks for `items` of a warp each: one an item, up to a few times what the
+// SMs hold at once (more only repeat what a warp sets up once).  0: no device.
+unsigned item_grid(long long items, int warps) {
+  return static_cast<unsigned>(std::min<long long>((items + warps - 1) / warps, 16LL * sm_count()));
+}
+
 template <int D, bool ROPE>
 int launch_append8(const attn::RopeTable& table, const attn::Append8Params& p, cudaStream_t stream) {
-  const long long warps = p.total_q;
-  const unsigned grid = static_cast<unsigned>((warps * 32 + attn::kAppend8Threads - 1) / attn::kAppend8Threads);
+  constexpr int rows = 512 / D;  // of a warp's pass
+  const long long groups = (ROPE ? (p.Hq + rows * attn::kRopeRows - 1) / (rows * attn::kRopeRows) : 0) +
+                           (p.Hkv + rows * attn::kRopeRows / 2 - 1) / (rows * attn::kRopeRows / 2);
+  const unsigned grid = item_grid(p.total_q * groups, attn::kAppend8Threads / 32);
+  if (grid == 0) return fail_cuda(cudaErrorInvalidDevice);
   attn::append8_kernel<D, ROPE><<<grid, attn::kAppend8Threads, 0, stream>>>(table, p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
@@ -234,7 +243,9 @@ int attn_rope(const attn_bf16* q, attn_bf16* q_out, const long long* q_strides, 
   p.B = B;
   p.N = N;
   p.sign = inverse ? -1.f : 1.f;
-  const unsigned grid = static_cast<unsigned>((tokens * 32 + attn::kRopeThreads - 1) / attn::kRopeThreads);
+  const long long rows = 512 / d * attn::kRopeRows;  // of an item
+  const unsigned grid = item_grid(tokens * ((static_cast<long long>(p.q.H) + p.k.H + rows - 1) / rows), attn::kRopeThreads / 32);
+  if (grid == 0) return fail_cuda(cudaErrorInvalidDevice);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 128)
     attn::rope_kernel<128><<<grid, attn::kRopeThreads, 0, s>>>(table, p);

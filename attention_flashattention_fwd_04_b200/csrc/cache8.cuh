@@ -69,79 +69,109 @@ struct Append8Params {
 
 constexpr int kAppend8Threads = 128;
 
-// One warp a token; lanes as in rope_kernel.  A row's largest magnitude is a
-// reduction over its D / 16 lanes; with ROPE, q and k are turned first and k is
-// quantised from the 32-bit result (one rounding, not two).
+// Items of a warp: a token and either kRopeRows passes over its queries or
+// kRopeRows / 2 passes over its KV heads, keys and values; lanes as in
+// rope_kernel.  A row's largest magnitude is a reduction over its D / 16 lanes.
+// With ROPE, q and k are turned first and k is quantised from the 32-bit result
+// (one rounding, not two).
 template <int D, bool ROPE>
 __global__ void __launch_bounds__(kAppend8Threads)
     append8_kernel(const __grid_constant__ RopeTable table, const Append8Params p) {
-  constexpr int kLanes = D / 16;
-  constexpr int kRows = 32 / kLanes;
-  const int t = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-  if (t >= p.total_q) return;
-  const int lane = threadIdx.x & 31;
-  const int s = warp_find_sequence(p.cu_q, p.num_seqs, t);
-  const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1], len = p.seq_lens[s];
-  if (t >= q1) return;  // padding behind the last sequence
-  const int nq = q1 - q0;
-  int page = -1, slot = 0;
-  if (t >= q0 && nq <= len && len <= p.max_pages * p.page_size) {
-    const int pos = len - nq + (t - q0);
-    page = p.block_table[static_cast<size_t>(s) * p.max_pages + pos / p.page_size];
-    slot = pos % p.page_size;
-  }
-  if (page < 0 || page >= p.num_pages) {
-    if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
-    return;
-  }
-  const int l = lane % kLanes;
-  const RopeLane rl = rope_lane(l, ROPE ? table.half : 0, ROPE && table.adjacent);
-  float2 cs[8];
-  if (ROPE && rl.turns) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPairs = kRopeRows / 2;
+  __shared__ __align__(16) float2 angles[ROPE ? kAppend8Threads / 32 : 1][kRopeMaxHalf];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q_groups = ROPE ? (p.Hq + kRows * kRopeRows - 1) / (kRows * kRopeRows) : 0;
+  const int groups = q_groups + (p.Hkv + kRows * kPairs - 1) / (kRows * kPairs);
+  const long long items = static_cast<long long>(p.total_q) * groups;
+  const RopeLane rl = rope_lane(lane % kLanes, ROPE ? table.half : 0, ROPE && table.adjacent);
+  RopeFreq freq;
+  if (ROPE) freq = rope_freq(table, lane);
+  int s = -1, q0 = 0, q1 = 0, len = 0;  // the sequence of the last item, often this one's too
+  for (long long item = static_cast<long long>(blockIdx.x) * (kAppend8Threads / 32) + warp; item < items;
+       item += static_cast<long long>(gridDim.x) * (kAppend8Threads / 32)) {
+    const int t = static_cast<int>(item / groups), group = static_cast<int>(item - static_cast<long long>(t) * groups);
+    const bool of_q = ROPE && group < q_groups;
+    // Rows: queries u, or key u / 2 (u even) and value u / 2 (u odd).
+    const int h0 = lane / kLanes + (of_q ? group * kRows * kRopeRows : (group - q_groups) * kRows * kPairs);
+    uint4 v[kRopeRows][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      cs[i] = rope_cos_sin(p.positions[static_cast<long long>(table.axis[rl.freq + i]) * p.total_q + t],
-                           table.turn[rl.freq + i]);
-  }
-  const int nqh = ROPE ? p.Hq : 0;
-  const int rows = nqh + 2 * p.Hkv;
-  for (int r0 = 0; r0 < rows; r0 += kRows) {
-    const int r = r0 + lane / kLanes;
-    const bool on = r < rows;
-    const bool is_q = r < nqh, is_k = !is_q && r < nqh + p.Hkv;
-    const int h = is_q ? r : is_k ? r - nqh : r - nqh - p.Hkv;
-    const __nv_bfloat16* src = is_q ? p.q + (static_cast<size_t>(t) * p.Hq + h) * D
-                                    : (is_k ? p.k_new : p.v_new) + (static_cast<size_t>(t) * p.Hkv + h) * D;
-    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-    if (on) {
-      v0 = *reinterpret_cast<const uint4*>(src + rl.off0);
-      v1 = *reinterpret_cast<const uint4*>(src + rl.off1);
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int h = h0 + (of_q ? u : u / 2) * kRows, H = of_q ? p.Hq : p.Hkv;
+      const __nv_bfloat16* src = (of_q ? p.q : u % 2 == 0 ? p.k_new : p.v_new) + (static_cast<size_t>(t) * H + h) * D;
+      v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < H) {
+        v[u][0] = *reinterpret_cast<const uint4*>(src + rl.off0);
+        v[u][1] = *reinterpret_cast<const uint4*>(src + rl.off1);
+      }
     }
-    float x[8], y[8];
-    unpack_bf16x8(v0, x);
-    unpack_bf16x8(v1, y);
-    if (ROPE && rl.turns && (is_q || is_k)) rope_turn(x, y, cs, table.adjacent);
-    if (is_q) {
-      __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(t) * p.Hq + h) * D;
-      *reinterpret_cast<uint4*>(dst + rl.off0) = rl.turns ? pack_bf16x8(x) : v0;
-      *reinterpret_cast<uint4*>(dst + rl.off1) = rl.turns ? pack_bf16x8(y) : v1;
+    if (s < 0 || t < q0 || t >= q1) {
+      s = warp_find_sequence(p.cu_q, p.num_seqs, t);
+      q0 = p.cu_q[s];
+      q1 = p.cu_q[s + 1];
+      len = p.seq_lens[s];
     }
-    float amax = 0.f;
+    if (t >= q1) continue;  // padding behind the last sequence
+    int page = -1, slot = 0;
+    if (t >= q0 && q1 - q0 <= len && len <= p.max_pages * p.page_size) {
+      const int pos = len - (q1 - t);
+      const int i = pos / p.page_size;
+      page = p.block_table[static_cast<size_t>(s) * p.max_pages + i];
+      slot = pos - i * p.page_size;
+    }
+    float2 cs[8];
+    if (ROPE) {
+      rope_angles<D>(freq, p.positions + t, p.total_q, table.half, 1.f, angles[ROPE ? warp : 0], lane);
+      rope_take(angles[ROPE ? warp : 0], rl, cs);
+    }
+    if (page < 0 || page >= p.num_pages) {
+      if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+      continue;
+    }
+    if (of_q) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+      for (int u = 0; u < kRopeRows; ++u) {
+        const int h = h0 + u * kRows;
+        if (h >= p.Hq) continue;
+        if (rl.turns) {
+          float x[8], y[8];
+          unpack_bf16x8(v[u][0], x);
+          unpack_bf16x8(v[u][1], y);
+          rope_turn(x, y, cs, table.adjacent);
+          v[u][0] = pack_bf16x8(x);
+          v[u][1] = pack_bf16x8(y);
+        }
+        __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(t) * p.Hq + h) * D;
+        *reinterpret_cast<uint4*>(dst + rl.off0) = v[u][0];
+        *reinterpret_cast<uint4*>(dst + rl.off1) = v[u][1];
+      }
+      continue;
+    }
+    const size_t at = (static_cast<size_t>(page) * p.page_size + slot) * p.Hkv;
+    uint32_t scales = 0;
 #pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if (on && !is_q) {
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int h = h0 + u / 2 * kRows;
+      float x[8], y[8];
+      unpack_bf16x8(v[u][0], x);
+      unpack_bf16x8(v[u][1], y);
+      if (ROPE && u % 2 == 0 && rl.turns) rope_turn(x, y, cs, table.adjacent);
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
       const int e = cache8_exponent(amax);
       const float m = cache8_pow2(-e);
-      uint8_t* dst = (is_k ? p.k_pool : p.v_pool) + ((static_cast<size_t>(page) * p.page_size + slot) * p.Hkv + h) * D;
+      scales = u % 2 == 0 ? e + 127 : scales | (e + 127) << 8;
+      if (h >= p.Hkv) continue;
+      uint8_t* dst = (u % 2 == 0 ? p.k_pool : p.v_pool) + (at + h) * D;
       *reinterpret_cast<uint2*>(dst + rl.off0) = make_uint2(pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m),
                                                             pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
       *reinterpret_cast<uint2*>(dst + rl.off1) = make_uint2(pack_e4m3x4(y[0] * m, y[1] * m, y[2] * m, y[3] * m),
                                                             pack_e4m3x4(y[4] * m, y[5] * m, y[6] * m, y[7] * m));
-      if (l == 0)
-        p.kv_scales[((static_cast<size_t>(page) * p.Hkv + h) * p.page_size + slot) * 2 + (is_k ? 0 : 1)] =
-            static_cast<uint8_t>(e + 127);
+      if (u % 2 == 1 && lane % kLanes == 0)
+        *reinterpret_cast<uint16_t*>(p.kv_scales + ((static_cast<size_t>(page) * p.Hkv + h) * p.page_size + slot) * 2) =
+            static_cast<uint16_t>(scales);
     }
   }
 }

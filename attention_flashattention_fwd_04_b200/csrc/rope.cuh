@@ -113,46 +113,106 @@ struct RopeParams {
   float sign;             // -1: the gradient
 };
 
+// Kernels that turn rows work in items, a warp each: a token and up to
+// kRopeRows passes over its heads, 32 / (D / 16) rows a pass.  All of an item's
+// rows are requested first; its angles are worked out while they are under way,
+// each once, by one lane, and handed round in shared memory.
 constexpr int kRopeThreads = 128;
+constexpr int kRopeRows = 4;
 
-// One warp a token: its lanes take D / 16 of a row each and go through the
-// token's heads, queries then keys.
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
-  constexpr int kLanes = D / 16;
-  constexpr int kRows = 32 / kLanes;
-  const long long token = (static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
-  if (token >= static_cast<long long>(p.B) * p.N) return;
-  const int lane = threadIdx.x & 31;
-  const int b = static_cast<int>(token / p.N), n = static_cast<int>(token % p.N);
-  const RopeLane rl = rope_lane(lane % kLanes, table.half, table.adjacent);
-  float2 cs[8];
-  if (rl.turns) {
+// A lane's frequencies in a warp: `lane`, and `lane` + 32 where there are so many.
+struct RopeFreq {
+  uint64_t turn[2];
+  int axis[2];
+};
+
+__device__ __forceinline__ RopeFreq rope_freq(const RopeTable& table, int lane) {
+  RopeFreq f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pos = p.positions[static_cast<long long>(table.axis[rl.freq + i]) * p.B * p.N + token];
-      cs[i] = rope_cos_sin(pos, table.turn[rl.freq + i]);
-      cs[i].y *= p.sign;
+  for (int i = 0; i < 2; ++i) {
+    f.turn[i] = table.turn[lane + 32 * i];
+    f.axis[i] = table.axis[lane + 32 * i];
+  }
+  return f;
+}
+
+// cos and sin of a token's angles, to `cs` (shared memory of the warp).
+template <int D>
+__device__ __forceinline__ void rope_angles(const RopeFreq& f, const int32_t* positions, long long axis_stride, int half, float sign,
+                                            float2* cs, int lane) {
+  int pos[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) pos[i] = lane + 32 * i < half ? positions[f.axis[i] * axis_stride] : 0;
+  __syncwarp();  // the last item's have been read
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    if (lane + 32 * i < half) {
+      float2 v = rope_cos_sin(pos[i], f.turn[i]);
+      v.y *= sign;
+      cs[lane + 32 * i] = v;
     }
   }
-  for (int r = lane / kLanes; r < p.q.H + p.k.H; r += kRows) {
-    const bool is_q = r < p.q.H;
-    const RopeTensor& t = is_q ? p.q : p.k;
-    const int h = is_q ? r : r - p.q.H;
-    const __nv_bfloat16* src = t.x + b * t.b + h * t.h + n * t.n;
-    __nv_bfloat16* dst = t.out + b * t.ob + h * t.oh + n * t.on;
-    uint4 v0 = *reinterpret_cast<const uint4*>(src + rl.off0);
-    uint4 v1 = *reinterpret_cast<const uint4*>(src + rl.off1);
-    if (rl.turns) {
-      float x[8], y[8];
-      unpack_bf16x8(v0, x);
-      unpack_bf16x8(v1, y);
-      rope_turn(x, y, cs, table.adjacent);
-      v0 = pack_bf16x8(x);
-      v1 = pack_bf16x8(y);
+  __syncwarp();
+}
+
+// The lane's 8 angles.
+__device__ __forceinline__ void rope_take(const float2* cs, const RopeLane& rl, float2 (&out)[8]) {
+  if (!rl.turns) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(cs + rl.freq)[i];
+    out[2 * i] = make_float2(v.x, v.y);
+    out[2 * i + 1] = make_float2(v.z, v.w);
+  }
+}
+
+// Items: (token, group of kRopeRows * 32 / (D / 16) heads, queries then keys).
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  __shared__ __align__(16) float2 angles[kRopeThreads / 32][kRopeMaxHalf];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = p.q.H + p.k.H, groups = (rows + kRows * kRopeRows - 1) / (kRows * kRopeRows);
+  const long long tokens = static_cast<long long>(p.B) * p.N, items = tokens * groups;
+  const RopeLane rl = rope_lane(lane % kLanes, table.half, table.adjacent);
+  const RopeFreq freq = rope_freq(table, lane);
+  for (long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + warp; item < items;
+       item += static_cast<long long>(gridDim.x) * (kRopeThreads / 32)) {
+    const long long token = item / groups;
+    const int r0 = static_cast<int>(item - token * groups) * kRows * kRopeRows + lane / kLanes;
+    const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(b) * p.N);
+    uint4 v[kRopeRows][2];
+    __nv_bfloat16* dst[kRopeRows];
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      const int r = r0 + u * kRows;
+      const bool is_q = r < p.q.H;
+      const RopeTensor& t = is_q ? p.q : p.k;
+      const int h = is_q ? r : r - p.q.H;
+      dst[u] = r < rows ? t.out + b * t.ob + h * t.oh + n * t.on : nullptr;
+      if (r < rows) {
+        const __nv_bfloat16* src = t.x + b * t.b + h * t.h + n * t.n;
+        v[u][0] = *reinterpret_cast<const uint4*>(src + rl.off0);
+        v[u][1] = *reinterpret_cast<const uint4*>(src + rl.off1);
+      }
     }
-    *reinterpret_cast<uint4*>(dst + rl.off0) = v0;
-    *reinterpret_cast<uint4*>(dst + rl.off1) = v1;
+    rope_angles<D>(freq, p.positions + token, tokens, table.half, p.sign, angles[warp], lane);
+    float2 cs[8];
+    rope_take(angles[warp], rl, cs);
+#pragma unroll
+    for (int u = 0; u < kRopeRows; ++u) {
+      if (dst[u] == nullptr) continue;
+      if (rl.turns) {
+        float x[8], y[8];
+        unpack_bf16x8(v[u][0], x);
+        unpack_bf16x8(v[u][1], y);
+        rope_turn(x, y, cs, table.adjacent);
+        v[u][0] = pack_bf16x8(x);
+        v[u][1] = pack_bf16x8(y);
+      }
+      *reinterpret_cast<uint4*>(dst[u] + rl.off0) = v[u][0];
+      *reinterpret_cast<uint4*>(dst[u] + rl.off1) = v[u][1];
+    }
   }
 }
 
