@@ -65,43 +65,54 @@ struct Append8Params {
   const int32_t* seq_lens;     // [num_seqs], after the append
   const int32_t* block_table;  // [num_seqs, max_pages]
   int num_seqs, total_q, Hq, Hkv, page_size, max_pages, num_pages;
+  int tokens_log2;             // of a block
 };
 
-constexpr int kAppend8Threads = 128;
+// Largest magnitude of a row that LANES lanes hold, 16 values each (NaN aside).
+template <int LANES>
+__device__ __forceinline__ float row_amax(const float (&x)[8], const float (&y)[8]) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  return amax;
+}
 
-// Items of a warp: a token and either kRopeRows passes over its queries or
-// kRopeRows / 2 passes over its KV heads, keys and values; lanes as in
-// rope_kernel.  A row's largest magnitude is a reduction over its D / 16 lanes.
-// With ROPE, q and k are turned first and k is quantised from the 32-bit result
-// (one rounding, not two).
-template <int D, bool ROPE>
-__global__ void __launch_bounds__(kAppend8Threads)
-    append8_kernel(const __grid_constant__ RopeTable table, const Append8Params p) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPairs = kRopeRows / 2;
-  __shared__ __align__(16) float2 angles[ROPE ? kAppend8Threads / 32 : 1][kRopeMaxHalf];
+__device__ __forceinline__ uint2 cache8_codes(const float (&x)[8], float m) {
+  return make_uint2(pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m), pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
+}
+
+constexpr int kAppend8Threads = 128;
+constexpr int kAppend8Heads = 1;  // passes of an item
+
+// Items of a warp: a token and kAppend8Heads passes over its KV heads, keys and
+// values; D / 16 lanes a row as in rope_kernel.  All of an item's rows are
+// requested before its place in the cache is looked up.
+template <int D>
+__global__ void __launch_bounds__(kAppend8Threads) append8_kernel(const Append8Params p) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q_groups = ROPE ? (p.Hq + kRows * kRopeRows - 1) / (kRows * kRopeRows) : 0;
-  const int groups = q_groups + (p.Hkv + kRows * kPairs - 1) / (kRows * kPairs);
+  const int groups = (p.Hkv + kRows * kAppend8Heads - 1) / (kRows * kAppend8Heads);
   const long long items = static_cast<long long>(p.total_q) * groups;
-  const RopeLane rl = rope_lane(lane % kLanes, ROPE ? table.half : 0, ROPE && table.adjacent);
-  RopeFreq freq;
-  if (ROPE) freq = rope_freq(table, lane);
+  const int off = 8 * (lane % kLanes);  // 8 values there and 8 at D / 2 behind: whole lines a pass
   int s = -1, q0 = 0, q1 = 0, len = 0;  // the sequence of the last item, often this one's too
   for (long long item = static_cast<long long>(blockIdx.x) * (kAppend8Threads / 32) + warp; item < items;
        item += static_cast<long long>(gridDim.x) * (kAppend8Threads / 32)) {
     const int t = static_cast<int>(item / groups), group = static_cast<int>(item - static_cast<long long>(t) * groups);
-    const bool of_q = ROPE && group < q_groups;
-    // Rows: queries u, or key u / 2 (u even) and value u / 2 (u odd).
-    const int h0 = lane / kLanes + (of_q ? group * kRows * kRopeRows : (group - q_groups) * kRows * kPairs);
-    uint4 v[kRopeRows][2];
+    const int h0 = lane / kLanes + group * kRows * kAppend8Heads;
+    uint4 v[kAppend8Heads][2][2];  // [pass][key, value][8 values]
 #pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int h = h0 + (of_q ? u : u / 2) * kRows, H = of_q ? p.Hq : p.Hkv;
-      const __nv_bfloat16* src = (of_q ? p.q : u % 2 == 0 ? p.k_new : p.v_new) + (static_cast<size_t>(t) * H + h) * D;
-      v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < H) {
-        v[u][0] = *reinterpret_cast<const uint4*>(src + rl.off0);
-        v[u][1] = *reinterpret_cast<const uint4*>(src + rl.off1);
+    for (int u = 0; u < kAppend8Heads; ++u) {
+      const int h = h0 + u * kRows;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const __nv_bfloat16* src = (kv == 0 ? p.k_new : p.v_new) + (static_cast<size_t>(t) * p.Hkv + h) * D + off;
+        v[u][kv][0] = v[u][kv][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < p.Hkv) {
+          v[u][kv][0] = reinterpret_cast<const uint4*>(src)[0];
+          v[u][kv][1] = reinterpret_cast<const uint4*>(src)[D / 16];
+        }
       }
     }
     if (s < 0 || t < q0 || t >= q1) {
@@ -118,59 +129,117 @@ __global__ void __launch_bounds__(kAppend8Threads)
       page = p.block_table[static_cast<size_t>(s) * p.max_pages + i];
       slot = pos - i * p.page_size;
     }
-    float2 cs[8];
-    if (ROPE) {
-      rope_angles<D>(freq, p.positions + t, p.total_q, table.half, 1.f, angles[ROPE ? warp : 0], lane);
-      rope_take(angles[ROPE ? warp : 0], rl, cs);
-    }
     if (page < 0 || page >= p.num_pages) {
       if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
       continue;
     }
-    if (of_q) {
-#pragma unroll
-      for (int u = 0; u < kRopeRows; ++u) {
-        const int h = h0 + u * kRows;
-        if (h >= p.Hq) continue;
-        if (rl.turns) {
-          float x[8], y[8];
-          unpack_bf16x8(v[u][0], x);
-          unpack_bf16x8(v[u][1], y);
-          rope_turn(x, y, cs, table.adjacent);
-          v[u][0] = pack_bf16x8(x);
-          v[u][1] = pack_bf16x8(y);
-        }
-        __nv_bfloat16* dst = p.q_out + (static_cast<size_t>(t) * p.Hq + h) * D;
-        *reinterpret_cast<uint4*>(dst + rl.off0) = v[u][0];
-        *reinterpret_cast<uint4*>(dst + rl.off1) = v[u][1];
-      }
-      continue;
-    }
     const size_t at = (static_cast<size_t>(page) * p.page_size + slot) * p.Hkv;
-    uint32_t scales = 0;
 #pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int h = h0 + u / 2 * kRows;
-      float x[8], y[8];
-      unpack_bf16x8(v[u][0], x);
-      unpack_bf16x8(v[u][1], y);
-      if (ROPE && u % 2 == 0 && rl.turns) rope_turn(x, y, cs, table.adjacent);
-      float amax = 0.f;
+    for (int u = 0; u < kAppend8Heads; ++u) {
+      const int h = h0 + u * kRows;
+      uint32_t scales = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-      const int e = cache8_exponent(amax);
-      const float m = cache8_pow2(-e);
-      scales = u % 2 == 0 ? e + 127 : scales | (e + 127) << 8;
-      if (h >= p.Hkv) continue;
-      uint8_t* dst = (u % 2 == 0 ? p.k_pool : p.v_pool) + (at + h) * D;
-      *reinterpret_cast<uint2*>(dst + rl.off0) = make_uint2(pack_e4m3x4(x[0] * m, x[1] * m, x[2] * m, x[3] * m),
-                                                            pack_e4m3x4(x[4] * m, x[5] * m, x[6] * m, x[7] * m));
-      *reinterpret_cast<uint2*>(dst + rl.off1) = make_uint2(pack_e4m3x4(y[0] * m, y[1] * m, y[2] * m, y[3] * m),
-                                                            pack_e4m3x4(y[4] * m, y[5] * m, y[6] * m, y[7] * m));
-      if (u % 2 == 1 && lane % kLanes == 0)
+      for (int kv = 0; kv < 2; ++kv) {
+        float x[8], y[8];
+        unpack_bf16x8(v[u][kv][0], x);
+        unpack_bf16x8(v[u][kv][1], y);
+        const int e = cache8_exponent(row_amax<kLanes>(x, y));
+        scales |= static_cast<uint32_t>(e + 127) << (8 * kv);
+        if (h < p.Hkv) {
+          const float m = cache8_pow2(-e);
+          uint2* dst = reinterpret_cast<uint2*>((kv == 0 ? p.k_pool : p.v_pool) + (at + h) * D + off);
+          dst[0] = cache8_codes(x, m);
+          dst[D / 16] = cache8_codes(y, m);
+        }
+      }
+      if (h < p.Hkv && lane % kLanes == 0)
         *reinterpret_cast<uint16_t*>(p.kv_scales + ((static_cast<size_t>(page) * p.Hkv + h) * p.page_size + slot) * 2) =
+            static_cast<uint16_t>(scales);
+    }
+  }
+}
+
+// A block's tokens, threads and angles are those of rope_kernel.  A row's largest
+// magnitude is a reduction over its D / 16 lanes; a thread takes a head's key and
+// value, so that both scales go in one store.  k is quantised from the 32-bit
+// result of the rotation (one rounding, not two).
+template <int D>
+__global__ void __launch_bounds__(kRowThreads, 2) rope_append8_kernel(const __grid_constant__ RopeTable table, const Append8Params p) {
+  using R = RowShape<D>;
+  __shared__ __align__(16) float2 angles[kRowTokens][kRopeMaxHalf];
+  __shared__ int pages[kRowTokens], slots[kRowTokens];  // page: -1 for a token that is left out
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int step = R::kSlots >> p.tokens_log2;  // heads at a time
+  const int first = static_cast<int>(blockIdx.x) << p.tokens_log2;
+  const int tokens = min(1 << p.tokens_log2, p.total_q - first);
+  const int slot = threadIdx.x / R::kLanes;
+  const int tok = slot / step, h0 = slot % step;
+  const RopeLane rl = rope_lane(threadIdx.x % R::kLanes, table.half, table.adjacent);
+  const bool in = tok < tokens;
+  const size_t t = static_cast<size_t>(first) + tok;
+  uint4 v[2][kRowBatch][2];
+  rows_load(v[0], p.q + t * p.Hq * D, D, h0, step, in ? p.Hq : 0, rl);
+  rope_angles(table, p.positions + first, p.total_q, tokens, 1.f, angles);
+  // Where each token goes, a warp a token.
+  for (int i = warp; i < tokens; i += kRowThreads / 32) {
+    const int row = first + i, s = warp_find_sequence(p.cu_q, p.num_seqs, row);
+    const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1], len = p.seq_lens[s];
+    int page = -1;
+    if (row < q1) {  // else padding behind the last sequence
+      if (row >= q0 && q1 - q0 <= len && len <= p.max_pages * p.page_size) {
+        const int pos = len - (q1 - row), at = pos / p.page_size;
+        page = p.block_table[static_cast<size_t>(s) * p.max_pages + at];
+        if (lane == 0) slots[i] = pos - at * p.page_size;
+      }
+      if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+        page = -1;
+      }
+    }
+    if (lane == 0) pages[i] = page;
+  }
+  __syncthreads();
+  const int page = in ? pages[tok] : -1, at_slot = page >= 0 ? slots[tok] : 0;
+  const bool on = page >= 0;
+  const int hq = on ? p.Hq : 0, hk = on ? p.Hkv : 0;
+  float2 cs[8];
+  const int more = kRowBatch * step;
+  rope_take(angles[tok], rl, cs);
+  const __nv_bfloat16* q = p.q + t * p.Hq * D;
+  __nv_bfloat16* q_out = p.q_out + t * p.Hq * D;
+  for (int h = h0; h < hq; h += 2 * more) {
+    rows_load(v[1], q, D, h + more, step, hq, rl);
+    rows_turn(v[0], q_out, D, h, step, hq, rl, cs, table.adjacent);
+    rows_load(v[0], q, D, h + 2 * more, step, hq, rl);
+    rows_turn(v[1], q_out, D, h + more, step, hq, rl, cs, table.adjacent);
+  }
+  // Keys and values: all lanes of a warp go round together (the reductions).
+  const size_t row0 = (static_cast<size_t>(max(page, 0)) * p.page_size + at_slot) * p.Hkv;
+  for (int h1 = 0; h1 < p.Hkv; h1 += more) {
+    const int hb = h1 + h0;
+    rows_load(v[0], p.k_new + t * p.Hkv * D, D, hb, step, hk, rl);
+    rows_load(v[1], p.v_new + t * p.Hkv * D, D, hb, step, hk, rl);
+#pragma unroll
+    for (int u = 0; u < kRowBatch; ++u) {
+      if (h1 + u * step >= p.Hkv) break;
+      const int h = hb + u * step;
+      uint32_t scales = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x[8], y[8];
+        unpack_bf16x8(v[i][u][0], x);
+        unpack_bf16x8(v[i][u][1], y);
+        if (i == 0 && rl.turns) rope_turn(x, y, cs, table.adjacent);
+        const int e = cache8_exponent(row_amax<R::kLanes>(x, y));
+        const float m = cache8_pow2(-e);
+        scales |= static_cast<uint32_t>(e + 127) << (8 * i);
+        if (h >= hk) continue;
+        uint8_t* dst = (i == 0 ? p.k_pool : p.v_pool) + (row0 + h) * D;
+        *reinterpret_cast<uint2*>(dst + rl.off0) = cache8_codes(x, m);
+        *reinterpret_cast<uint2*>(dst + rl.off1) = cache8_codes(y, m);
+      }
+      if (h < hk && threadIdx.x % R::kLanes == 0)
+        *reinterpret_cast<uint16_t*>(p.kv_scales + ((static_cast<size_t>(page) * p.Hkv + h) * p.page_size + at_slot) * 2) =
             static_cast<uint16_t>(scales);
     }
   }

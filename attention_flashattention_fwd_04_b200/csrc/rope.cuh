@@ -110,52 +110,43 @@ struct RopeParams {
   RopeTensor q, k;        // k.H = 0: no keys
   const int32_t* positions;  // [axes, B, N]
   int B, N;
+  int tokens_log2;        // of a block
+  int tokens_together;    // a head's tokens are nearer to one another than a token's heads
   float sign;             // -1: the gradient
 };
 
-// Kernels that turn rows work in items, a warp each: a token and up to
-// kRopeRows passes over its heads, 32 / (D / 16) rows a pass.  All of an item's
-// rows are requested first; its angles are worked out while they are under way,
-// each once, by one lane, and handed round in shared memory.
-constexpr int kRopeThreads = 128;
-constexpr int kRopeRows = 4;
+// The kernels on rows (this one and the append to the 8-bit cache) give a block
+// 2^tokens_log2 tokens.  Their angles are worked out once, by all threads, into
+// shared memory, while the first rows are on their way; then a thread keeps to
+// one token, its 16 values of a row and their angles, and goes through the heads.
+// The block's D / 16 lanes a row cover kRowSlots rows at a time: heads of one
+// token next to one another, or tokens of one head (whichever lie together).
+constexpr int kRowThreads = 256;
+constexpr int kRowTokens = 16;  // most tokens of a block
+constexpr int kRowBatch = 4;    // rows that a thread has under way
 
-// A lane's frequencies in a warp: `lane`, and `lane` + 32 where there are so many.
-struct RopeFreq {
-  uint64_t turn[2];
-  int axis[2];
+template <int D>
+struct RowShape {
+  static constexpr int kLanes = D / 16;
+  static constexpr int kSlots = kRowThreads / kLanes;
 };
 
-__device__ __forceinline__ RopeFreq rope_freq(const RopeTable& table, int lane) {
-  RopeFreq f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f.turn[i] = table.turn[lane + 32 * i];
-    f.axis[i] = table.axis[lane + 32 * i];
+// cos and sin of the block's angles, [token][frequency].  kRowThreads is a
+// multiple of kRopeMaxHalf, so a thread has one frequency.
+__device__ __forceinline__ void rope_angles(const RopeTable& table, const int32_t* positions, long long axis_stride, int tokens,
+                                            float sign, float2 (*cs)[kRopeMaxHalf]) {
+  const int j = threadIdx.x % kRopeMaxHalf;
+  if (j >= table.half) return;
+  const uint64_t turn = table.turn[j];
+  const int32_t* mine = positions + table.axis[j] * axis_stride;
+  for (int t = threadIdx.x / kRopeMaxHalf; t < tokens; t += kRowThreads / kRopeMaxHalf) {
+    float2 v = rope_cos_sin(mine[t], turn);
+    v.y *= sign;
+    cs[t][j] = v;
   }
-  return f;
 }
 
-// cos and sin of a token's angles, to `cs` (shared memory of the warp).
-template <int D>
-__device__ __forceinline__ void rope_angles(const RopeFreq& f, const int32_t* positions, long long axis_stride, int half, float sign,
-                                            float2* cs, int lane) {
-  int pos[D / 64];
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) pos[i] = lane + 32 * i < half ? positions[f.axis[i] * axis_stride] : 0;
-  __syncwarp();  // the last item's have been read
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    if (lane + 32 * i < half) {
-      float2 v = rope_cos_sin(pos[i], f.turn[i]);
-      v.y *= sign;
-      cs[lane + 32 * i] = v;
-    }
-  }
-  __syncwarp();
-}
-
-// The lane's 8 angles.
+// A lane's 8 angles.
 __device__ __forceinline__ void rope_take(const float2* cs, const RopeLane& rl, float2 (&out)[8]) {
   if (!rl.turns) return;
 #pragma unroll
@@ -166,53 +157,72 @@ __device__ __forceinline__ void rope_take(const float2* cs, const RopeLane& rl, 
   }
 }
 
-// Items: (token, group of kRopeRows * 32 / (D / 16) heads, queries then keys).
+// Loads up to kRowBatch rows: heads h, h + step, ...
+__device__ __forceinline__ void rows_load(uint4 (&v)[kRowBatch][2], const __nv_bfloat16* x, long long stride, int h, int step, int H,
+                                          const RopeLane& rl) {
+#pragma unroll
+  for (int u = 0; u < kRowBatch; ++u) {
+    if (h + u * step < H) {
+      const __nv_bfloat16* src = x + (h + u * step) * stride;
+      v[u][0] = *reinterpret_cast<const uint4*>(src + rl.off0);
+      v[u][1] = *reinterpret_cast<const uint4*>(src + rl.off1);
+    }
+  }
+}
+
+// Turns them and stores them.
+__device__ __forceinline__ void rows_turn(uint4 (&v)[kRowBatch][2], __nv_bfloat16* out, long long stride, int h, int step, int H,
+                                          const RopeLane& rl, const float2 (&cs)[8], bool adjacent) {
+#pragma unroll
+  for (int u = 0; u < kRowBatch; ++u) {
+    if (h + u * step >= H) continue;
+    if (rl.turns) {
+      float x[8], y[8];
+      unpack_bf16x8(v[u][0], x);
+      unpack_bf16x8(v[u][1], y);
+      rope_turn(x, y, cs, adjacent);
+      v[u][0] = pack_bf16x8(x);
+      v[u][1] = pack_bf16x8(y);
+    }
+    __nv_bfloat16* dst = out + (h + u * step) * stride;
+    *reinterpret_cast<uint4*>(dst + rl.off0) = v[u][0];
+    *reinterpret_cast<uint4*>(dst + rl.off1) = v[u][1];
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  __shared__ __align__(16) float2 angles[kRopeThreads / 32][kRopeMaxHalf];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.q.H + p.k.H, groups = (rows + kRows * kRopeRows - 1) / (kRows * kRopeRows);
-  const long long tokens = static_cast<long long>(p.B) * p.N, items = tokens * groups;
-  const RopeLane rl = rope_lane(lane % kLanes, table.half, table.adjacent);
-  const RopeFreq freq = rope_freq(table, lane);
-  for (long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + warp; item < items;
-       item += static_cast<long long>(gridDim.x) * (kRopeThreads / 32)) {
-    const long long token = item / groups;
-    const int r0 = static_cast<int>(item - token * groups) * kRows * kRopeRows + lane / kLanes;
-    const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<long long>(b) * p.N);
-    uint4 v[kRopeRows][2];
-    __nv_bfloat16* dst[kRopeRows];
-#pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      const int r = r0 + u * kRows;
-      const bool is_q = r < p.q.H;
-      const RopeTensor& t = is_q ? p.q : p.k;
-      const int h = is_q ? r : r - p.q.H;
-      dst[u] = r < rows ? t.out + b * t.ob + h * t.oh + n * t.on : nullptr;
-      if (r < rows) {
-        const __nv_bfloat16* src = t.x + b * t.b + h * t.h + n * t.n;
-        v[u][0] = *reinterpret_cast<const uint4*>(src + rl.off0);
-        v[u][1] = *reinterpret_cast<const uint4*>(src + rl.off1);
-      }
-    }
-    rope_angles<D>(freq, p.positions + token, tokens, table.half, p.sign, angles[warp], lane);
-    float2 cs[8];
-    rope_take(angles[warp], rl, cs);
-#pragma unroll
-    for (int u = 0; u < kRopeRows; ++u) {
-      if (dst[u] == nullptr) continue;
-      if (rl.turns) {
-        float x[8], y[8];
-        unpack_bf16x8(v[u][0], x);
-        unpack_bf16x8(v[u][1], y);
-        rope_turn(x, y, cs, table.adjacent);
-        v[u][0] = pack_bf16x8(x);
-        v[u][1] = pack_bf16x8(y);
-      }
-      *reinterpret_cast<uint4*>(dst[u] + rl.off0) = v[u][0];
-      *reinterpret_cast<uint4*>(dst[u] + rl.off1) = v[u][1];
-    }
+__global__ void __launch_bounds__(kRowThreads, 2) rope_kernel(const __grid_constant__ RopeTable table, const RopeParams p) {
+  using R = RowShape<D>;
+  __shared__ __align__(16) float2 angles[kRowTokens][kRopeMaxHalf];
+  const int per_block = 1 << p.tokens_log2, step = R::kSlots >> p.tokens_log2;  // heads at a time
+  const long long first = static_cast<long long>(blockIdx.x) << p.tokens_log2, all = static_cast<long long>(p.B) * p.N;
+  const int tokens = static_cast<int>(min(static_cast<long long>(per_block), all - first));
+  const int slot = threadIdx.x / R::kLanes;
+  const int tok = p.tokens_together ? slot & (per_block - 1) : slot / step;
+  const int h0 = p.tokens_together ? slot >> p.tokens_log2 : slot % step;
+  const RopeLane rl = rope_lane(threadIdx.x % R::kLanes, table.half, table.adjacent);
+  const bool on = tok < tokens;
+  const long long token = first + tok;
+  const long long b = token / p.N, n = token - b * p.N;
+  const int hq = on ? p.q.H : 0, hk = on ? p.k.H : 0;  // a thread behind the last token has no rows
+  const __nv_bfloat16 *q = p.q.x + b * p.q.b + n * p.q.n, *k = p.k.x + b * p.k.b + n * p.k.n;
+  __nv_bfloat16 *q_out = p.q.out + b * p.q.ob + n * p.q.on, *k_out = p.k.out + b * p.k.ob + n * p.k.on;
+  uint4 v[2][kRowBatch][2];
+  rows_load(v[0], q, p.q.h, h0, step, hq, rl);
+  rope_angles(table, p.positions + first, all, tokens, p.sign, angles);
+  __syncthreads();
+  float2 cs[8];
+  rope_take(angles[tok], rl, cs);
+  const int more = kRowBatch * step;
+  for (int h = h0; h < hq; h += 2 * more) {
+    rows_load(v[1], q, p.q.h, h + more, step, hq, rl);
+    rows_turn(v[0], q_out, p.q.oh, h, step, hq, rl, cs, table.adjacent);
+    rows_load(v[0], q, p.q.h, h + 2 * more, step, hq, rl);
+    rows_turn(v[1], q_out, p.q.oh, h + more, step, hq, rl, cs, table.adjacent);
+  }
+  for (int h = h0; h < hk; h += more) {
+    rows_load(v[0], k, p.k.h, h, step, hk, rl);
+    rows_turn(v[0], k_out, p.k.oh, h, step, hk, rl, cs, table.adjacent);
   }
 }
 
