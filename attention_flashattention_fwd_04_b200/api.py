@@ -1,22 +1,24 @@
 """ctypes binding over the C ABI in ``include/attn_b200.h``.
 
 Argument marshalling only: every step of the attention runs in the CUDA
-kernels of ``libattn_b200.so``.  PyTorch supplies device memory (outputs,
+kernels of ``libattn_b200.so``.  The calls of the rotary positions and of the
+8-bit cache marshal theirs in C++ (``_attn_torch.so``), which a small decode step
+feels.  PyTorch supplies device memory (outputs,
 workspace) and the current stream.  There is no CPU or PyTorch fallback: if
 the library is missing or a call fails, this module raises.
 """
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
+import importlib.util
 import os
 import re
 
 import torch
 
-from .build import INCLUDE, LIB_PATH
+from .build import INCLUDE, LIB_PATH, TORCH_PATH
 
 ATTN_OK = 0
 _STATUS_NAMES = {
@@ -664,95 +666,65 @@ def rope_spec(d: int, sections=None, theta: float = 10000.0, rot_dim: int | None
     return spec
 
 
-def _one_device(tensors, names):
-    """Checks, after the shapes, that the tensors (None left out) are on one
-    CUDA device; returns its index."""
-    index = tensors[0].get_device()
-    for t, name in zip(tensors, names):
-        if t is not None and (t.get_device() != index or index < 0):
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            raise ValueError(f"{name} is on {t.device}, not on {tensors[0].device}")
-    return index
+_marshal = None
 
 
-_HERE = contextlib.nullcontext()
+def _marshaller():
+    """The C++ argument marshalling (loaded on first use), bound to the functions of lib()."""
+    global _marshal
+    if _marshal is None:
+        if not os.path.exists(TORCH_PATH):
+            raise RuntimeError(
+                f"{TORCH_PATH} is missing: build it with "
+                "`python -m attention_flashattention_fwd_04_b200.build`")
+        names = ("attn_rope", "paged_kv_append_fp8", "paged_rope_append_fp8", "paged_kv_gather_fp8",
+                 "paged_attn_decode_fp8_workspace_bytes", "paged_attn_decode_fp8")
+        addresses = [ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names]
+        spec = importlib.util.spec_from_file_location("_attn_torch", TORCH_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*addresses)
+        _marshal = module
+    return _marshal
 
 
-def _launch_on(index, stream):
-    """(context, stream handle) of a call on device ``index``: the given
-    stream, which must be one of that device, or its current stream.  What the
-    call allocates inside the context belongs to that stream, so that it is not
-    handed out again while the call may still use it."""
-    if stream is not None:
-        if stream.device.index != index:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
-        return torch.cuda.stream(stream), stream.cuda_stream
-    here = _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
-    return here, torch.cuda.current_stream(index).cuda_stream
+def _on_stream(fn):
+    """Gives a call its ``stream``: current while the call runs, so that what it
+    allocates belongs to that stream and is not handed out again while the
+    kernels may still use it."""
+    @functools.wraps(fn)
+    def wrapped(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        for a in args:
+            if isinstance(a, torch.Tensor) and a.is_cuda and a.device != stream.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {a.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return wrapped
 
 
-def _rope_tensor(x, name, out, out_name):
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != torch.bfloat16 or x.dim() not in (3, 4):
-        raise ValueError(f"{name} must be a 3-d or 4-d bfloat16 tensor, got {x.dtype} {tuple(x.shape)}")
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != x.shape):
-        raise ValueError(f"{out_name} must be a bfloat16 tensor of {name}'s shape")
-    for t, what in ((x, name), (out, out_name)):
-        if t is not None and t.stride(-1) != 1 and t.numel():
-            raise ValueError(f"the rows of {what} must be contiguous")
-
-
-def _rope_strides(x):
-    """{batch, head, token} strides of [B, H, N, d] or packed [T, H, d]."""
-    s = x.stride()
-    return (ctypes.c_longlong * 3)(s[0], s[1], s[2]) if x.dim() == 4 else (ctypes.c_longlong * 3)(0, s[1], s[0])
-
-
+@_on_stream
 def attn_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, spec: RopeSpec, inverse: bool = False,
-              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
     """Rotary positions with several axes on queries and keys.
 
     q [B,Hq,N,d] and k [B,Hkv,N,d] bf16 with positions [axes,B,N] int32, or
     packed q [T,Hq,d], k [T,Hkv,d] with positions [axes,T]; ``k`` may be None.
     Rows must be contiguous, the other strides are free (multiples of 8).
     ``inverse`` turns back, which is the gradient.  ``q_out`` / ``k_out`` may be
-    q / k.  Returns (q_out, k_out), bf16."""
-    _rope_tensor(q, "q", q_out, "q_out")
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-    else:
-        _rope_tensor(k, "k", k_out, "k_out")
-    if q.dim() == 4:
-        B, Hq, N, d = q.shape
-        where = (B, N)
-    else:
-        N, Hq, d = q.shape
-        B, where = 1, (N,)
-    if k is not None:
-        Hkv = k.shape[1]
-        if k.shape != ((B, Hkv, N, d) if q.dim() == 4 else (N, Hkv, d)):
-            raise ValueError(f"k shape {tuple(k.shape)} does not match q {tuple(q.shape)}")
+    q / k.  ``stream``: a torch.cuda.Stream (default: the current one).
+    Returns (q_out, k_out), bf16."""
+    rc, q_out, k_out = (_marshal or _marshaller()).rope(q, k, positions, _spec_address(spec), inverse, q_out, k_out)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope")
+    return q_out, k_out
+
+
+def _spec_address(spec) -> int:
     if not isinstance(spec, RopeSpec):
         raise TypeError("spec must come from rope_spec")
-    _require(positions, "positions", torch.int32, 1 + len(where), cuda=False)
-    if positions.shape != (spec.num_axes, *where):
-        raise ValueError(f"positions must be {(spec.num_axes, *where)}, got {tuple(positions.shape)}")
-    here, handle = _launch_on(_one_device((q, k, positions, q_out, k_out), ("q", "k", "positions", "q_out", "k_out")), stream)
-    with here:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        has_k = k is not None
-        rc = lib().attn_rope(q.data_ptr(), q_out.data_ptr(), _rope_strides(q), _rope_strides(q_out), Hq,
-                             k.data_ptr() if has_k else None, k_out.data_ptr() if has_k else None,
-                             _rope_strides(k) if has_k else None, _rope_strides(k_out) if has_k else None,
-                             Hkv if has_k else 0, B, N, d, positions.data_ptr(), ctypes.byref(spec), int(bool(inverse)), handle)
-    _check(rc, "attn_rope")
-    return q_out, k_out
+    return ctypes.addressof(spec)
 
 
 # ----------------------------------------------------------------------------
@@ -766,130 +738,48 @@ def kv_cache_fp8(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda"
     return pools[0], pools[1], scales.view(torch.float8_e8m0fnu)
 
 
-_CACHE8 = ("k_pool", "v_pool", "kv_scales", "block_table", "seq_lens")
-_CACHE8_TYPES = (torch.float8_e4m3fn, torch.float8_e4m3fn, torch.float8_e8m0fnu)
-
-
-def _cache8_args(cache, more, names, types, dims):
-    """Types and shapes shared by the calls on the 8-bit cache, before any CUDA
-    call.  ``cache``: the tensors named in _CACHE8; ``more``: the call's others
-    (or None), with their names, types and numbers of dimensions.  Returns (S,
-    num_pages, page_size, Hkv, d, max_pages)."""
-    k_pool, v_pool, kv_scales, block_table, seq_lens = cache
-    for t, name, kind in zip(cache, _CACHE8, _CACHE8_TYPES):
-        _require(t, name, torch.uint8 if isinstance(t, torch.Tensor) and t.dtype is torch.uint8 else kind, 4, cuda=False)
-    _require(block_table, "block_table", torch.int32, 2, cuda=False)
-    _require(seq_lens, "seq_lens", torch.int32, 1, cuda=False)
-    for t, name, kind, nd in zip(more, names, types, dims):
-        if t is not None:
-            _require(t, name, kind, nd, cuda=False)
-    shape = k_pool.shape
-    num_pages, page_size, Hkv, d = shape
-    if v_pool.shape != shape:
-        raise ValueError(f"v_pool shape {tuple(v_pool.shape)} differs from k_pool's {tuple(shape)}")
-    if kv_scales.shape != (num_pages, Hkv, page_size, 2):
-        raise ValueError(f"kv_scales must be {(num_pages, Hkv, page_size, 2)}, got {tuple(kv_scales.shape)}")
-    S, max_pages = block_table.shape
-    if seq_lens.shape[0] != S:
-        raise ValueError(f"block_table {tuple(block_table.shape)} does not have one row per sequence ({seq_lens.shape[0]})")
-    return S, num_pages, page_size, Hkv, d, max_pages
-
-
-def _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d):
-    if k_new.shape[1:] != (Hkv, d) or v_new.shape != k_new.shape:
-        raise ValueError(f"k_new {tuple(k_new.shape)} / v_new {tuple(v_new.shape)} do not match the pools")
-    if cu_seqlens_q.shape[0] != seq_lens.shape[0] + 1:
-        raise ValueError("cu_seqlens_q does not match the number of sequences")
-
-
+@_on_stream
 def paged_kv_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                         kv_scales: torch.Tensor, block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
-                        seq_lens: torch.Tensor, stream=None):
+                        seq_lens: torch.Tensor):
     """paged_kv_append into an 8-bit cache: quantises the new rows (packed
     [total_q,Hkv,d] bf16) as they are written.  k_pool / v_pool
     [num_pages,page_size,Hkv,d] float8_e4m3fn and kv_scales
     [num_pages,Hkv,page_size,2] float8_e8m0fnu (uint8 views of them are taken
-    too), see kv_cache_fp8.  In place."""
-    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (k_new, v_new, cu_seqlens_q)
-    names = ("k_new", "v_new", "cu_seqlens_q")
-    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        cache, more, names, (torch.bfloat16, torch.bfloat16, torch.int32), (3, 3, 1))
-    _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
-    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
-    with here:
-        rc = lib().paged_kv_append_fp8(k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                                       kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-                                       block_table.data_ptr(), S, k_new.shape[0], Hkv, d, page_size, max_pages, num_pages,
-                                       handle)
-    _check(rc, "paged_kv_append_fp8")
+    too), see kv_cache_fp8.  In place.  ``stream`` as in attn_rope."""
+    rc = (_marshal or _marshaller()).append(k_new, v_new, k_pool, v_pool, kv_scales, block_table, cu_seqlens_q, seq_lens)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_kv_append_fp8")
 
 
+@_on_stream
 def paged_rope_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, positions: torch.Tensor,
                           spec: RopeSpec, k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor,
                           block_table: torch.Tensor, cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor,
-                          q_out: torch.Tensor | None = None, stream=None):
+                          q_out: torch.Tensor | None = None):
     """attn_rope on a step's q [total_q,Hq,d] and k_new and
     paged_kv_append_fp8, in one kernel (positions [axes,total_q] int32).  The
-    cache is updated in place; ``q_out`` may be q.  Returns q_out; its rows
-    behind cu_seqlens_q[-1] are not written."""
-    if not isinstance(spec, RopeSpec):
-        raise TypeError("spec must come from rope_spec")
-    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (q, k_new, v_new, q_out, positions, cu_seqlens_q)
-    names = ("q", "k_new", "v_new", "q_out", "positions", "cu_seqlens_q")
-    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        cache, more, names, (torch.bfloat16,) * 4 + (torch.int32,) * 2, (3, 3, 3, 3, 2, 1))
-    _append8_shapes(k_new, v_new, cu_seqlens_q, seq_lens, Hkv, d)
-    total_q, Hq = q.shape[:2]
-    if q.shape != (k_new.shape[0], Hq, d) or (q_out is not None and q_out.shape != q.shape):
-        raise ValueError("q / q_out do not match k_new")
-    if positions.shape != (spec.num_axes, total_q):
-        raise ValueError(f"positions must be {(spec.num_axes, total_q)}, got {tuple(positions.shape)}")
-    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
-    with here:
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        rc = lib().paged_rope_append_fp8(q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
-                                         positions.data_ptr(), ctypes.byref(spec), k_pool.data_ptr(), v_pool.data_ptr(),
-                                         kv_scales.data_ptr(), cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-                                         block_table.data_ptr(), S, total_q, Hq, Hkv, d, page_size, max_pages, num_pages,
-                                         handle)
-    _check(rc, "paged_rope_append_fp8")
+    cache is updated in place; ``q_out`` may be q.  ``stream`` as in attn_rope.
+    Returns q_out; its rows behind cu_seqlens_q[-1] are not written."""
+    rc, q_out = (_marshal or _marshaller()).rope_append(q, k_new, v_new, positions, _spec_address(spec), k_pool, v_pool, kv_scales,
+                                                        block_table, cu_seqlens_q, seq_lens, q_out)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_rope_append_fp8")
     return q_out
 
 
+@_on_stream
 def paged_kv_gather_fp8(k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor, block_table: torch.Tensor,
                         seq_lens: torch.Tensor, cu_seqlens_k: torch.Tensor, total_rows: int | None = None,
-                        k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+                        k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
     """Read an 8-bit cache back as bf16 rows (exact): token t of sequence s
     goes to row cu_seqlens_k[s] + t of k_out / v_out [total_rows,Hkv,d].  Give
     the outputs, or ``total_rows`` to have them made (rows that no token falls
-    on are then undefined).  Returns (k_out, v_out)."""
-    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (cu_seqlens_k, k_out, v_out)
-    names = ("cu_seqlens_k", "k_out", "v_out")
-    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        cache, more, names, (torch.int32, torch.bfloat16, torch.bfloat16), (1, 3, 3))
-    if cu_seqlens_k.shape[0] != S + 1:
-        raise ValueError("cu_seqlens_k does not match the number of sequences")
-    if (k_out is None) != (v_out is None):
-        raise ValueError("give both k_out and v_out, or neither")
-    if k_out is not None:
-        rows = k_out.shape[0]
-        if k_out.shape != (rows, Hkv, d) or v_out.shape != k_out.shape or total_rows not in (None, rows):
-            raise ValueError(f"k_out / v_out must be [rows, {Hkv}, {d}] alike, got {tuple(k_out.shape)} / "
-                             f"{tuple(v_out.shape)}")
-    elif total_rows is None or total_rows < 0:
-        raise ValueError("total_rows (or k_out and v_out) is needed")
-    else:
-        rows = int(total_rows)
-    here, handle = _launch_on(_one_device(cache + more, _CACHE8 + names), stream)
-    with here:
-        if k_out is None:
-            k_out = torch.empty((rows, Hkv, d), dtype=torch.bfloat16, device=k_pool.device)
-            v_out = torch.empty_like(k_out)
-        rc = lib().paged_kv_gather_fp8(k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
-                                       seq_lens.data_ptr(), cu_seqlens_k.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), S,
-                                       rows, Hkv, d, page_size, max_pages, num_pages, handle)
-    _check(rc, "paged_kv_gather_fp8")
+    on are then undefined).  ``stream`` as in attn_rope.  Returns (k_out, v_out)."""
+    rc, k_out, v_out = (_marshal or _marshaller()).gather(k_pool, v_pool, kv_scales, block_table, seq_lens, cu_seqlens_k, total_rows,
+                                                          k_out, v_out)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_kv_gather_fp8")
     return k_out, v_out
 
 
@@ -897,41 +787,17 @@ def paged_attn_decode_fp8_workspace_bytes(num_seqs: int, Hq: int, Hkv: int, d: i
     return int(lib().paged_attn_decode_fp8_workspace_bytes(num_seqs, Hq, Hkv, d, max_pages, page_size))
 
 
+@_on_stream
 def paged_attn_decode_fp8(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, kv_scales: torch.Tensor,
                           block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float | None = None,
                           workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                          lse: torch.Tensor | None = None, stream=None):
+                          lse: torch.Tensor | None = None):
     """paged_attn_decode over an 8-bit cache (see paged_kv_append_fp8).
 
     q [S,Hq,d] bf16; block_table [S,max_pages] int32; seq_lens [S] int32, 0
-    giving O = 0 and LSE = -inf.  Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32)."""
-    cache, more = (k_pool, v_pool, kv_scales, block_table, seq_lens), (q, out, lse)
-    names = ("q", "out", "lse")
-    S, num_pages, page_size, Hkv, d, max_pages = _cache8_args(
-        cache, more, names, (torch.bfloat16, torch.bfloat16, torch.float32), (3, 3, 2))
-    Hq = q.shape[1]
-    if q.shape != (S, Hq, d):
-        raise ValueError(f"q must be [{S}, Hq, {d}], got {tuple(q.shape)}")
-    if out is not None and out.shape != q.shape:
-        raise ValueError(f"out shape {tuple(out.shape)} differs from q's {tuple(q.shape)}")
-    if lse is not None and lse.shape != (S, Hq):
-        raise ValueError(f"lse shape {tuple(lse.shape)} is not ({S}, {Hq})")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    if scale is None:
-        scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
-    here, handle = _launch_on(_one_device(cache + more + (workspace,), _CACHE8 + names + ("workspace",)), stream)
-    with here:
-        if workspace is None:
-            need = lib().paged_attn_decode_fp8_workspace_bytes(S, Hq, Hkv, d, max_pages, page_size)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
-        rc = lib().paged_attn_decode_fp8(
-            q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), page_size, out.data_ptr(), lse.data_ptr(), S, Hq, Hkv, d, max_pages, num_pages,
-            float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
-    _check(rc, "paged_attn_decode_fp8")
+    giving O = 0 and LSE = -inf.  ``scale`` defaults to 1 / sqrt(d); ``stream``
+    as in attn_rope.  Returns (o [S,Hq,d] bf16, lse [S,Hq] fp32)."""
+    rc, out, lse = (_marshal or _marshaller()).decode(q, k_pool, v_pool, kv_scales, block_table, seq_lens, scale, workspace, out, lse)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_attn_decode_fp8")
     return out, lse
