@@ -102,6 +102,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint4 lds_128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -184,8 +190,9 @@ __device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, i
 template <int D, int NT>
 struct Decode8Warp {
   float acc[NT][D / 16][4];  // O^T: values 16 c + grp (0, 1) and + 8 (2, 3) of heads 2 tig (+ 1)
-  float m[NT][2], l[NT][2];  // of heads 2 tig (+ 1); l is this lane's share
-  float f[NT][2];            // scores' factor
+  // Of heads 2 tig (low) and 2 tig + 1 (high): minus the bound, this lane's share
+  // of the sum, the scores' factor.
+  uint64_t nm[NT], l[NT], f[NT];
   uint32_t q[NT][D / 16][2];
 
   __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig) {
@@ -216,16 +223,16 @@ struct Decode8Warp {
         q[nt][i][1] = pack_f16x2(__uint_as_float(raw[i].y << 16) * up, __uint_as_float(raw[i].y & 0xffff0000u) * up);
       }
       const float factor = scale_log2 * __int_as_float((127 - shift) << 23);  // of head grp; wanted: of heads 2 tig (+ 1)
-      f[nt][0] = __shfl_sync(0xffffffffu, factor, 8 * tig);
-      f[nt][1] = __shfl_sync(0xffffffffu, factor, 8 * tig + 4);
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      f[nt] = f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4));
+      nm[nt] = f2_pack(INFINITY, INFINITY);
+      l[nt] = 0;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
     }
   }
 
-  // valid: the tokens of the 16 that belong to the sequence.
+  // valid: the tokens of the 16 that belong to the sequence (TAIL: fewer than 16).
+  template <bool TAIL>
   __device__ __forceinline__ void tile(uint32_t k, uint32_t v, uint32_t scales, int valid, int lane) {
     const int grp = lane >> 2, tig = lane & 3;
     const int t0 = decode8_token(grp), t1 = t0 + 2;  // tokens of rows grp and grp + 8
@@ -245,7 +252,7 @@ struct Decode8Warp {
         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt], a0, a1, a2, a3, q[nt][4 * j + i][0], q[nt][4 * j + i][1]);
       }
     }
-    if (valid < 16) {
+    if (TAIL && valid < 16) {
       // Tokens past the end may hold NaN codes, and 0 * NaN is NaN: their
       // values are cleared (their scores below).
       for (int i = lane; i < (16 - valid) * (D / 16); i += 32)
@@ -256,52 +263,72 @@ struct Decode8Warp {
       __syncwarp();
     }
     const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
+    // K's scales, and V's exponents + 6 as floats (a byte in the last bits of 2^23).
     const float k0 = cache8_scale(e0 & 255u), k1 = cache8_scale(e1 & 255u);
-    // The exponents of V as floats: a byte in the last bits of 2^23.
-    float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388735.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388735.f;
-    bool up = false;
-    float t[NT][4];
+    const float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388729.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388729.f;
+    const uint64_t k00 = f2_pack(k0, k0), k11 = f2_pack(k1, k1), v00 = f2_pack(v0, v0), v11 = f2_pack(v1, v1);
+    uint64_t x[NT][2];  // scores of rows grp and grp + 8 but for f
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool out = (e < 2 ? t0 : t1) >= valid;
-        sc[nt][e] = out ? -INFINITY : sc[nt][e] * ((e < 2 ? k0 : k1) * f[nt][e & 1]);
-        t[nt][e] = out ? -INFINITY : sc[nt][e] + (e < 2 ? v0 : v1);
-        up |= t[nt][e] > m[nt][e & 1] + 8.f;
-      }
+      x[nt][0] = f2_mul(f2_pack(sc[nt][0], sc[nt][1]), k00);
+      x[nt][1] = f2_mul(f2_pack(sc[nt][2], sc[nt][3]), k11);
     }
-    if (__any_sync(0xffffffffu, up)) {  // a new bound: the largest so far
+    // x f + add for both rows, -inf past the end: a select, since what the slots
+    // there hold, their scales too, may be NaN.
+    auto scores = [&](int nt, uint64_t add0, uint64_t add1, float (&out)[4]) {
+      f2_unpack(f2_fma(x[nt][0], f[nt], add0), out[0], out[1]);
+      f2_unpack(f2_fma(x[nt][1], f[nt], add1), out[2], out[3]);
+      if (TAIL) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = (e < 2 ? t0 : t1) < valid ? out[e] : -INFINITY;
+      }
+    };
+    float w[NT][4];  // log2 of the weights, 2^6 up
+    float top = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      scores(nt, f2_add(v00, nm[nt]), f2_add(v11, nm[nt]), w[nt]);
+      top = max3(top, max3(w[nt][0], w[nt][1], w[nt][2]), w[nt][3]);
+    }
+    if (__any_sync(0xffffffffu, top > 14.f)) {  // more than 2^8 off the bound (or none yet): a new one, the largest so far
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        float s[4], m[2], a[2];
+        scores(nt, v00, v11, s);
+        f2_unpack(nm[nt], m[0], m[1]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(t[nt][u], t[nt][u + 2]);
+          float mx = fmaxf(s[u], s[u + 2]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx, m[nt][u]);
-          const float a = ex2_approx(m[nt][u] - mx);
-          m[nt][u] = mx;
-          l[nt][u] *= a;
+          mx = fmaxf(mx - 6.f, -m[u]);
+          a[u] = ex2_approx(-m[u] - mx);
+          m[u] = -mx;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            acc[nt][c][u] *= a;
-            acc[nt][c][u + 2] *= a;
+            acc[nt][c][u] *= a[u];
+            acc[nt][c][u + 2] *= a[u];
           }
         }
+        nm[nt] = f2_pack(m[0], m[1]);
+        l[nt] = f2_mul(l[nt], f2_pack(a[0], a[1]));
+        scores(nt, f2_add(v00, nm[nt]), f2_add(v11, nm[nt]), w[nt]);
       }
     }
     uint32_t p[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
+      float s[4];
+      scores(nt, nm[nt], nm[nt], s);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = ex2_approx(t[nt][e] - m[nt][e & 1] + 6.f);
-      l[nt][0] += ex2_approx(sc[nt][0] - m[nt][0]) + ex2_approx(sc[nt][2] - m[nt][0]);
-      l[nt][1] += ex2_approx(sc[nt][1] - m[nt][1]) + ex2_approx(sc[nt][3] - m[nt][1]);
-      p[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
-      p[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+      for (int e = 0; e < 4; ++e) {
+        w[nt][e] = ex2_approx(w[nt][e]);
+        s[e] = ex2_approx(s[e]);
+      }
+      l[nt] = f2_add(l[nt], f2_add(f2_pack(s[0], s[1]), f2_pack(s[2], s[3])));
+      p[nt][0] = movmatrix_trans(pack_f16x2(w[nt][0], w[nt][1]));
+      p[nt][1] = movmatrix_trans(pack_f16x2(w[nt][2], w[nt][3]));
     }
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
@@ -497,7 +524,12 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       if (!ok) continue;
       const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + warp) * 32;
       const int valid = len - tile * tokens - chunk * 16;
-      if (valid > 0) w.tile(k, k + L::kPool, sc, valid, lane);
+      // Two head tiles gain by a path without the selects; one loses more by the
+      // code's size and its registers (64 sequences, NT = 1: 104 against 101 us).
+      if (NT == 2 && valid >= 16)
+        w.template tile<false>(k, k + L::kPool, sc, 16, lane);
+      else if (valid > 0)
+        w.template tile<true>(k, k + L::kPool, sc, valid, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(st));
       if (++st == STAGES) {
@@ -509,12 +541,18 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     // ring's next NT places), one thread a head works out what each of the
     // head's warps counts, and all threads add up and write O, 8 values at a
     // time.
+    float bound[NT][2], sum[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      f2_unpack(w.nm[nt], bound[nt][0], bound[nt][1]);
+      f2_unpack(w.l[nt], sum[nt][0], sum[nt][1]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        bound[nt][u] = -bound[nt][u];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) w.l[nt][u] += __shfl_xor_sync(0xffffffffu, w.l[nt][u], off);
+        for (int off = 4; off < 32; off <<= 1) sum[nt][u] += __shfl_xor_sync(0xffffffffu, sum[nt][u], off);
+      }
+    }
     uint32_t place[NT];
     decode8_consumers_sync<32 * kDecode8Warps>();  // the last run's factors have been read
 #pragma unroll
@@ -536,8 +574,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       if (grp == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          join[warp * 16 + nt * 8 + 2 * tig + u] = w.m[nt][u];
-          join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = w.l[nt][u];
+          join[warp * 16 + nt * 8 + 2 * tig + u] = bound[nt][u];
+          join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = sum[nt][u];
         }
       }
     }
