@@ -80,6 +80,24 @@ int validate_cache8(const void* k_pool, const void* v_pool, const void* kv_scale
   return ATTN_OK;
 }
 
+// Launches a kernel that may begin while the one before it ends
+// (griddep_wait in rope.cuh).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid_x, grid_y);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Tokens of a block of the kernels on rows: 16, so that their angles are shared
 // by many rows and a head's tokens make long runs (4 x 16 + 16 heads x 2048
 // tokens of d = 128: 24.1 us, with 8 tokens 26.4), but few enough that small
@@ -92,20 +110,24 @@ int row_tokens_log2(long long tokens) {
 
 template <int D>
 int launch_append8(const attn::RopeTable& table, attn::Append8Params p, bool rope, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return fail_cuda(cudaErrorInvalidDevice);
+  cudaError_t e;
   if (rope) {
     p.tokens_log2 = row_tokens_log2(p.total_q);
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.total_q) + (1 << p.tokens_log2) - 1) >> p.tokens_log2);
-    attn::rope_append8_kernel<D><<<grid, attn::kRowThreads, 0, stream>>>(table, p);
+    p.one_wave = grid <= static_cast<unsigned>(sms);
+    e = launch_early(attn::rope_append8_kernel<D>, grid, 1, attn::kRowThreads, 0, stream, table, p);
   } else {
     // A warp an item, up to a few times what the SMs hold at once.
     constexpr int heads = 512 / D * attn::kAppend8Heads, warps = attn::kAppend8Threads / 32;
     const long long items = static_cast<long long>(p.total_q) * ((p.Hkv + heads - 1) / heads);
-    const int sms = sm_count();
-    if (sms <= 0) return fail_cuda(cudaErrorInvalidDevice);
     const unsigned grid = static_cast<unsigned>(std::min<long long>((items + warps - 1) / warps, 16LL * sms));
-    attn::append8_kernel<D><<<grid, attn::kAppend8Threads, 0, stream>>>(p);
+    p.one_wave = grid <= static_cast<unsigned>(sms);
+    e = launch_early(attn::append8_kernel<D>, grid, 1, attn::kAppend8Threads, 0, stream, p);
   }
-  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail_cuda(e);
+  e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
 }
 
@@ -201,24 +223,15 @@ int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Dec
   auto kernel = attn::decode8_split_kernel<D, NT, PER_SM, STAGES>;
   cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, PER_SM, STAGES>>(L::kAlloc);
   if (e != cudaSuccess) return fail_cuda(e);
-  kernel<<<static_cast<unsigned>(p.ctas), L::kThreads, L::kAlloc, stream>>>(tk, tv, p);
-  e = cudaGetLastError();
+  e = launch_early(kernel, static_cast<unsigned>(p.ctas), 1, L::kThreads, L::kAlloc, stream, tk, tv, p);
   if (e != cudaSuccess) return fail_cuda(e);
-  cudaLaunchConfig_t cfg = {};
   // With few sequences and heads there are many partial rows for each: 16
   // warps share a head's, else one warp takes them.
   const bool wide = p.ctas > 16LL * p.S * (p.Hkv / p.hb);
   const int heads = wide ? 1 : attn::kMerge8Warps;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.Hq + heads - 1) / heads), static_cast<unsigned>(p.S));
-  cfg.blockDim = dim3(32 * attn::kMerge8Warps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = wide ? cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D, 16>, p)
-           : cudaLaunchKernelEx(&cfg, attn::decode8_merge_kernel<D, 1>, p);
+  const unsigned gx = static_cast<unsigned>((p.Hq + heads - 1) / heads), gy = static_cast<unsigned>(p.S);
+  e = wide ? launch_early(attn::decode8_merge_kernel<D, 16>, gx, gy, 32 * attn::kMerge8Warps, 0, stream, p)
+           : launch_early(attn::decode8_merge_kernel<D, 1>, gx, gy, 32 * attn::kMerge8Warps, 0, stream, p);
   if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);

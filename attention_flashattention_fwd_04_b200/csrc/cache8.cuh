@@ -66,6 +66,7 @@ struct Append8Params {
   const int32_t* block_table;  // [num_seqs, max_pages]
   int num_seqs, total_q, Hq, Hkv, page_size, max_pages, num_pages;
   int tokens_log2;             // of a block
+  int one_wave;                // all blocks are on the SMs at once
 };
 
 // Largest magnitude of a row that LANES lanes hold, 16 values each (NaN aside).
@@ -96,6 +97,8 @@ __global__ void __launch_bounds__(kAppend8Threads) append8_kernel(const Append8P
   const int groups = (p.Hkv + kRows * kAppend8Heads - 1) / (kRows * kAppend8Heads);
   const long long items = static_cast<long long>(p.total_q) * groups;
   const int off = 8 * (lane % kLanes);  // 8 values there and 8 at D / 2 behind: whole lines a pass
+  if (p.one_wave) griddep_launch();
+  griddep_wait();
   int s = -1, q0 = 0, q1 = 0, len = 0;  // the sequence of the last item, often this one's too
   for (long long item = static_cast<long long>(blockIdx.x) * (kAppend8Threads / 32) + warp; item < items;
        item += static_cast<long long>(gridDim.x) * (kAppend8Threads / 32)) {
@@ -177,6 +180,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) rope_append8_kernel(const __gr
   const RopeLane rl = rope_lane(threadIdx.x % R::kLanes, table.half, table.adjacent);
   const bool in = tok < tokens;
   const size_t t = static_cast<size_t>(first) + tok;
+  if (p.one_wave) griddep_launch();
+  griddep_wait();
   uint4 v[2][kRowBatch][2];
   rows_load(v[0], p.q + t * p.Hq * D, D, h0, step, in ? p.Hq : 0, rl);
   rope_angles(table, p.positions + first, p.total_q, tokens, 1.f, angles);

@@ -352,8 +352,6 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
                          const Decode8Params p) {
   using L = Decode8Layout<D, STAGES>;
   constexpr int kDecode8Warps = L::kWarps;
-  // The merge may be launched once every CTA has begun; it waits for this grid.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -364,6 +362,20 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   int32_t* warp_sums = reinterpret_cast<int32_t*>(smem + L::kWarpSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens_log2 = kDecode8RowsLog2 - p.hb_log2, tokens = 1 << tokens_log2;  // of a tile
+
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < STAGES; ++st) {
+      mbar_init(full_bar(st), 1);
+      mbar_init(empty_bar(st), kDecode8Warps);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  griddep_wait();  // what the call reads and writes: only behind the kernels before it
+  // From here on the merge may be launched (it reads the lengths, then waits for
+  // this grid): not earlier, so that what it reads is behind those kernels too.
+  griddep_launch();
 
   // Tiles before each sequence: every consumer thread sums up a run of
   // lengths, the warps' sums follow.
@@ -390,14 +402,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     if (lane == 31) warp_sums[warp] = before;
     before -= own;
   }
-  if (threadIdx.x == 0) {
-    first[0] = 0;
-    for (int st = 0; st < STAGES; ++st) {
-      mbar_init(full_bar(st), 1);
-      mbar_init(empty_bar(st), kDecode8Warps);
-    }
-    fence_mbar_init();
-  }
+  if (threadIdx.x == 0) first[0] = 0;
   __syncthreads();
   if (warp < kDecode8Warps) {
     for (int w = 0; w < warp; ++w) before += warp_sums[w];
@@ -424,10 +429,6 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     // costs the copy engine as much as one of 16 KB): lanes 2 w and 2 w + 1
     // bring those of consumer w.
     const int w_hl = (lane >> 1) & (p.hb - 1), w_chunk = lane >> (1 + p.hb_log2);
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
     bool ok = true;
     int count = 0, st = 0;  // tiles issued, and the next one's place in the ring
     uint32_t phase = 1;     // of the empty barriers: the ring's first round finds every place free
@@ -643,6 +644,7 @@ constexpr int kMerge8Warps = 16;
 
 template <int D, int PER>
 __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const Decode8Params p) {
+  griddep_launch();  // all of this grid's CTAs are on the SMs by then: the next call may set itself up beside them
   constexpr int kPer = D / 32, kHeads = kMerge8Warps / PER;
   __shared__ float rows[PER > 1 ? kMerge8Warps : 1][D], bound[kMerge8Warps], sums[kMerge8Warps];
   __shared__ int tiles[2][kMerge8Warps];
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
     pieces = on ? c1 - c0 + 1 : 0;
     slot0 = 2 * static_cast<size_t>(c0);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  griddep_wait();
   if (n == 0) {  // no tokens (or a length that the split pass reported)
     if (on && part == 0) {
       if (lane < D / 8) reinterpret_cast<uint4*>(p.o + head * D)[lane] = make_uint4(0u, 0u, 0u, 0u);

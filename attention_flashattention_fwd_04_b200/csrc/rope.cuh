@@ -19,6 +19,13 @@ namespace attn {
 
 constexpr int kRopeMaxHalf = 64;  // frequencies: d <= 128
 
+// Programmatic launches.  A kernel launched with the stream-serialisation
+// attribute may begin once every CTA of the kernel before it has called
+// griddep_launch (or ended); griddep_wait then waits for that kernel's end, with
+// all it wrote visible.  Both return at once in a launch without the attribute.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct RopeTable {
   uint64_t turn[kRopeMaxHalf];  // inv_freq / 2 pi modulo 1, in units of 2^-64
   uint8_t axis[kRopeMaxHalf];
