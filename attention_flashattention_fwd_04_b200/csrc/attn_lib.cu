@@ -306,7 +306,7 @@ int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint
   if (misaligned4(cu_seqlens_k)) return ATTN_ERR_ALIGN;
   if (total_rows == 0) return ATTN_OK;
   if (!k_out || !v_out) return ATTN_ERR_NULL;
-  if (misaligned16(k_out) || misaligned16(v_out)) return ATTN_ERR_ALIGN;
+  if (((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) != 0) return ATTN_ERR_ALIGN;
   attn::Gather8Params p{};
   p.k_pool = k_pool;
   p.v_pool = v_pool;

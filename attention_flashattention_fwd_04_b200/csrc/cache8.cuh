@@ -264,7 +264,8 @@ struct Gather8Params {
 
 constexpr int kGather8Threads = 128;
 
-// Two e4m3 codes times 2^e as a pair of bf16 (exact; NaN codes stay NaN).
+// Two e4m3 codes (in the low half of a word) times 2^e as a pair of bf16 (exact;
+// NaN codes stay NaN).
 __device__ __forceinline__ uint32_t cache8_bf16x2(uint32_t codes16, float two_e) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes16)));
@@ -273,12 +274,24 @@ __device__ __forceinline__ uint32_t cache8_bf16x2(uint32_t codes16, float two_e)
   return pack_bf16x2(lo * two_e, hi * two_e);
 }
 
+// 16 codes as bf16 in one 32-byte store.
+__device__ __forceinline__ void cache8_store16(__nv_bfloat16* dst, const uint4& c, float e) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(cache8_bf16x2(c.x, e)),
+               "r"(cache8_bf16x2(c.x >> 16, e)), "r"(cache8_bf16x2(c.y, e)), "r"(cache8_bf16x2(c.y >> 16, e)),
+               "r"(cache8_bf16x2(c.z, e)), "r"(cache8_bf16x2(c.z >> 16, e)), "r"(cache8_bf16x2(c.w, e)),
+               "r"(cache8_bf16x2(c.w >> 16, e))
+               : "memory");
+}
+
 // The scale byte as a float.  0 and 255 are never written (e is limited), but
 // a slot that no token was written to may hold them: such a row's values mean
 // nothing, and 2^-127 or infinity serve as well as any.
 __device__ __forceinline__ float cache8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// One warp a row of the output (one token): 8 codes a lane and step.
+// One warp a row of the output (one token): 16 codes a lane, of keys and values,
+// and kGather8Batch of each under way.
+constexpr int kGather8Batch = 2;
+
 template <int D>
 __global__ void __launch_bounds__(kGather8Threads) gather8_kernel(const Gather8Params p) {
   const int row = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -302,15 +315,26 @@ __global__ void __launch_bounds__(kGather8Threads) gather8_kernel(const Gather8P
   const size_t src = (static_cast<size_t>(page) * p.page_size + slot) * p.Hkv * D;
   const size_t dst = static_cast<size_t>(row) * p.Hkv * D;
   const uint8_t* scales = p.kv_scales + (static_cast<size_t>(page) * p.Hkv * p.page_size + slot) * 2;
-  for (int i = lane * 8; i < p.Hkv * D; i += 256) {
-    const uint2 k = *reinterpret_cast<const uint2*>(p.k_pool + src + i);
-    const uint2 v = *reinterpret_cast<const uint2*>(p.v_pool + src + i);
-    const uint32_t e = *reinterpret_cast<const uint16_t*>(scales + static_cast<size_t>(i / D) * p.page_size * 2);
-    const float ke = cache8_scale(e & 255u), ve = cache8_scale(e >> 8);
-    *reinterpret_cast<uint4*>(p.k_out + dst + i) = make_uint4(cache8_bf16x2(k.x, ke), cache8_bf16x2(k.x >> 16, ke),
-                                                              cache8_bf16x2(k.y, ke), cache8_bf16x2(k.y >> 16, ke));
-    *reinterpret_cast<uint4*>(p.v_out + dst + i) = make_uint4(cache8_bf16x2(v.x, ve), cache8_bf16x2(v.x >> 16, ve),
-                                                              cache8_bf16x2(v.y, ve), cache8_bf16x2(v.y >> 16, ve));
+  for (int i0 = lane * 16; i0 < p.Hkv * D; i0 += 512 * kGather8Batch) {
+    uint4 k[kGather8Batch], v[kGather8Batch];
+    uint32_t e[kGather8Batch];
+#pragma unroll
+    for (int u = 0; u < kGather8Batch; ++u) {
+      const int i = i0 + 512 * u;
+      if (i < p.Hkv * D) {
+        k[u] = *reinterpret_cast<const uint4*>(p.k_pool + src + i);
+        v[u] = *reinterpret_cast<const uint4*>(p.v_pool + src + i);
+        e[u] = *reinterpret_cast<const uint16_t*>(scales + static_cast<size_t>(i / D) * p.page_size * 2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kGather8Batch; ++u) {
+      const int i = i0 + 512 * u;
+      if (i < p.Hkv * D) {
+        cache8_store16(p.k_out + dst + i, k[u], cache8_scale(e[u] & 255u));
+        cache8_store16(p.v_out + dst + i, v[u], cache8_scale(e[u] >> 8));
+      }
+    }
   }
 }
 

@@ -439,7 +439,7 @@ int paged_rope_append_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn
 /*
  * paged_kv_gather_fp8 -- reads the 8-bit cache back as bf16 (exact):
  *   k_out, v_out  [total_rows, Hkv, d] bf16: token t of sequence s goes to row
- *                 cu_seqlens_k[s] + t, 0 <= t < seq_lens[s]
+ *                 cu_seqlens_k[s] + t, 0 <= t < seq_lens[s]; 32-byte aligned
  *   cu_seqlens_k  [num_seqs + 1] int32, non-decreasing from 0, at most
  *                 total_rows; a sequence may have more room than tokens (rows
  *                 behind its tokens, and behind the last sequence, stay as they

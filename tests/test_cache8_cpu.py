@@ -197,7 +197,7 @@ def test_8bit_cache_calls_reject(lib, fn, kw, code):
     ("append", dict(vn=FAKE + 8), 3), ("step", dict(q=None), 1), ("step", dict(qo=None), 1), ("step", dict(pos=None), 1),
     ("step", dict(Hq=0), 2), ("step", dict(spec=_bad_spec(rot_dim=8)), 2), ("step", dict(qo=FAKE + 8), 3),
     ("step", dict(d=64, spec=_bad_spec(rot_dim=128)), 2),
-    ("gather", dict(ko=None), 1), ("gather", dict(vo=None), 1), ("gather", dict(ko=FAKE + 8), 3),
+    ("gather", dict(ko=None), 1), ("gather", dict(vo=None), 1), ("gather", dict(ko=FAKE + 8), 3), ("gather", dict(vo=FAKE + 16), 3),
     ("decode", dict(q=None), 1), ("decode", dict(o=None), 1), ("decode", dict(lse=None), 1), ("decode", dict(Hq=7), 2),
     ("decode", dict(scale=0.0), 2), ("decode", dict(scale=math.nan), 2), ("decode", dict(Hq=34), 5),
     ("decode", dict(ws=None), 4), ("decode", dict(wb=16), 4), ("decode", dict(ws=FAKE + 8), 3), ("decode", dict(q=FAKE + 2), 3),
