@@ -148,6 +148,9 @@ __device__ __forceinline__ void ldmatrix_b8_trans(uint32_t addr, uint32_t& r0, u
 // + 3, as columns 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9.
 __device__ __forceinline__ int decode8_token(int r) { return 4 * ((r & 7) >> 1) + 2 * (r >> 3) + (r & 1); }
 
+// Tiles (or chunks) of 2^log2 tokens that a length takes; no sum that could pass 2^31.
+__device__ __forceinline__ int decode8_count(int len, int log2) { return (len >> log2) + ((len & ((1 << log2) - 1)) != 0); }
+
 // CTA c of n takes total / n tiles, and one more if c < total % n.
 struct Decode8Share {
   int each, more;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
         if (blockIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
         len = 0;
       }
-      own += (len + tokens - 1) >> tokens_log2;
+      own += decode8_count(len, tokens_log2);
       first[s + 1] = own;
     }
     before = own;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       const Decode8Run run = decode8_run(first, p.S, groups, at, end);
       at += run.to - run.from;
       const int len = p.seq_lens[run.s];
-      const int chunk_end = min((len + 15) / 16, run.to * chunks_per_tile);
+      const int chunk_end = min(decode8_count(len, 4), run.to * chunks_per_tile);
       const int32_t* table = p.block_table + static_cast<size_t>(run.s) * p.max_pages;
       const int head = run.hg * p.hb;
       // Where 32 chunks lie, one a lane (page << 4 | chunk of the page); the
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
   const int tokens_log2 = kDecode8RowsLog2 - p.hb_log2, most = p.max_pages * p.page_size;
   auto tiles_of = [&](int i) {
     const int len = p.seq_lens[i];
-    return len < 0 || len > most ? 0 : (len + (1 << tokens_log2) - 1) >> tokens_log2;
+    return len < 0 || len > most ? 0 : decode8_count(len, tokens_log2);
   };
   int before = 0, all = 0;  // tiles of one group of heads: of the sequences before s, of all
   for (int i = threadIdx.x; i < p.S; i += 32 * kMerge8Warps) {

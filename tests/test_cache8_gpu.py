@@ -469,6 +469,61 @@ def test_decode_garbage_workspace_shared_pages_and_repeat():
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])  # the same sums in the same order
 
 
+def test_decode_empty_batch_and_single_token():
+    c = filled_case(76, [0, 0, 0], 2, 64, 16)
+    o, lse = run_decode(c, rows(77, 3, 4, 64), 0.1)
+    assert api.device_status() == 0 and not o.any() and torch.all(lse == -float("inf"))
+    c = filled_case(78, [1], 1, 64, 16)  # one token: its value row, and its score
+    q = rows(79, 1, 1, 64)
+    o, lse = run_decode(c, q, 0.1)
+    page = int(c["table"][0, 0])
+    want = oracle.dequantise(c["vp"][page, 0].numpy(), c["sc"][page, :, 0, 1].numpy())
+    assert np.array_equal(f64(o)[0], want)
+    assert_decoded(c, q, 0.1, o, lse)
+
+
+def test_decode_more_sequences_than_one_launch_takes():
+    """1500 sequences (1024 a launch), sharing pages, some empty."""
+    c = filled_case(100, [40, 17, 0, 33], 2, 64, 16)
+    S = 1500
+    pick = torch.arange(S) % 4
+    c["table"], c["lens"] = c["table"][pick].contiguous(), c["lens"][pick].contiguous()
+    q = rows(101, 4, 4, 64)[pick].contiguous()
+    q[1300:1304] = rows(102, 4, 4, 64)
+    o, lse = run_decode(c, q, 0.1)
+    assert api.device_status() == 0
+    for s0 in (0, 1020, 1300, 1496):
+        part = dict(c, table=c["table"][s0:s0 + 4], lens=c["lens"][s0:s0 + 4])
+        assert_decoded(part, q[s0:s0 + 4], 0.1, o[s0:s0 + 4], lse[s0:s0 + 4])
+    # runs begin elsewhere in other sequences, so sums group differently: equal but for roundings
+    assert torch.allclose(lse[:1024:4], lse[0].expand(256, -1), atol=1e-5, rtol=0)
+
+
+def test_pages_behind_two_gigabytes():
+    """Pools of more than 2^31 bytes: append to, read back from and attend to their last pages."""
+    num_pages, ps, Hkv, d = 140000, 16, 8, 128
+    kp, vp = (torch.empty(num_pages, ps, Hkv, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.empty(num_pages, Hkv, ps, 2, dtype=torch.uint8, device="cuda")
+    assert kp.numel() > 2 ** 31
+    last = torch.tensor([[num_pages - 1, num_pages - 5, num_pages - 2]], dtype=torch.int32)
+    k, v = rows(110, 40, Hkv, d), rows(111, 40, Hkv, d)
+    cu, lens = torch.tensor([0, 40], dtype=torch.int32), torch.tensor([40], dtype=torch.int32)
+    cache = kp, vp, sc, last.cuda()
+    api.paged_kv_append_fp8(k.cuda(), v.cuda(), *cache, cu.cuda(), lens.cuda())
+    at = [num_pages - 5, num_pages - 2, num_pages - 1]
+    small = dict(kp=kp[at].cpu(), vp=vp[at].cpu(), sc=sc[at].cpu(), table=torch.tensor([[2, 0, 1]], dtype=torch.int32), lens=lens, ps=ps,
+                 Hkv=Hkv)
+    ko, vo = api.paged_kv_gather_fp8(*cache, lens.cuda(), cu.cuda(), 40)
+    (wk, wv), = oracle.paged_gather8(small["kp"].numpy(), small["vp"].numpy(), small["sc"].numpy(), [[2, 0, 1]], [40], ps)
+    codes_k, e = oracle.quantise_rows(f64(k))
+    assert np.array_equal(wk, oracle.dequantise(codes_k, e + 127))
+    assert np.array_equal(f64(ko), wk) and np.array_equal(f64(vo), wv)
+    q = rows(112, 1, 32, d)
+    o, lse = api.paged_attn_decode_fp8(q.cuda(), *cache, lens.cuda(), 0.1)
+    assert api.device_status() == 0
+    assert_decoded(small, q, 0.1, o, lse)
+
+
 # ------------------------------------------------------- as they are used, together
 
 def test_serving_steps_together():
@@ -558,3 +613,73 @@ def test_calls_on_another_stream():
         qo, _ = api.attn_rope(qc, None, torch.zeros(3, 2, dtype=torch.int32, device="cuda"), spec)
     side.synchronize()
     assert torch.equal(qo, qc)
+
+
+def test_steps_back_to_back_equal_steps_apart():
+    """A chain of steps whose kernels may begin while the ones before them end gives, bit for bit, what the same steps give with
+    the device idle between them."""
+    S, Hq, Hkv, d, ps, width = 5, 16, 4, 128, 16, 40
+    spec = make_spec(d)
+    table = torch.randperm(S * width, generator=torch.Generator().manual_seed(120)).to(torch.int32).view(S, width).cuda()
+    one = torch.arange(S + 1, dtype=torch.int32).cuda()
+    steps = [tuple(rows(130 + 7 * i + j, S, h, d).cuda() for j, h in enumerate((Hq, Hkv, Hkv))) for i in range(40)]
+    start = torch.tensor([0, 15, 200, 555, 31], dtype=torch.int32).cuda()
+    results = []
+    for apart in (False, True):
+        kp, vp, sc = api.kv_cache_fp8(S * width, ps, Hkv, d)
+        lens, got = start.clone(), []
+        torch.cuda.synchronize()
+        for q, k, v in steps:
+            lens += 1
+            if apart:
+                torch.cuda.synchronize()
+            qo = api.paged_rope_append_fp8(q, k, v, lens.repeat(3, 1), spec, kp, vp, sc, table, one, lens)
+            if apart:
+                torch.cuda.synchronize()
+            got.append((qo, *api.paged_attn_decode_fp8(qo, kp, vp, sc, table, lens, 0.1)))
+            if apart:
+                torch.cuda.synchronize()
+            got.append(api.paged_attn_decode_fp8(got[-1][1], kp, vp, sc, table, lens, 0.1))  # reads what the merge wrote
+        torch.cuda.synchronize()
+        results.append(got)
+    assert api.device_status() == 0
+    for a, b in zip(*results):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_graphs_of_one_memory_pool_and_two_streams():
+    c, c2 = filled_case(140, [700, 33], 2, 128, 16), filled_case(141, [5, 900], 2, 128, 16)
+    args = []
+    for x, seed in ((c, 142), (c2, 143)):
+        kp, vp, sc = gpu_cache(x)
+        args.append((rows(seed, 2, 8, 128).cuda(), kp, vp, sc, x["table"].cuda(), x["lens"].cuda(), 0.1))
+    want = [api.paged_attn_decode_fp8(*a) for a in args]
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    torch.cuda.synchronize()
+    for g, a in zip(graphs, args):
+        with torch.cuda.graph(g, pool=graphs[0].pool() if outs else None):
+            outs.append(api.paged_attn_decode_fp8(*a))
+    for _ in range(5):
+        for g, w, o in zip(graphs, want, outs):
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[api.paged_attn_decode_fp8(*a, stream=s) for s, a in zip(streams, args)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for o, w in zip(pair, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+def test_unaligned_outputs_are_refused():
+    c = filled_case(144, [20], 1, 64, 16)
+    kp, vp, sc = gpu_cache(c)
+    buf = torch.empty(20 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    off = buf[8:].view(20, 1, 64)  # 16-byte aligned only
+    with pytest.raises(api.AttnError) as e:
+        api.paged_kv_gather_fp8(kp, vp, sc, c["table"].cuda(), c["lens"].cuda(), torch.tensor([0, 20], dtype=torch.int32).cuda(),
+                                k_out=off, v_out=torch.empty_like(off))
+    assert e.value.status == 3
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        api.paged_attn_decode_fp8(rows(1, 1, 2, 64), kp, vp, sc, c["table"].cuda(), c["lens"].cuda())
