@@ -193,7 +193,7 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   const int tokens = attn::kDecode8Rows / pl.hb;
   for (pl.box = 16; pl.box < tokens && page_size % (2 * pl.box) == 0;) pl.box *= 2;
   const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
-  if (tiles > INT_MAX) return false;
+  if (tiles + 3LL * attn::kDecode8MaxSeqs * (Hkv / pl.hb) > INT_MAX) return false;  // units of work, in 32 bits
   // Every CTA that the SMs hold at once (see paged_attn_decode_fp8), or one a tile.
   pl.ctas = static_cast<int>(std::min<long long>(tiles, d == 64 || group <= 8 ? 2 * 148 : 148));
   const size_t rows = 2 * static_cast<size_t>(pl.ctas) * pl.hb * group;

@@ -292,12 +292,14 @@ def test_decode_share_out(seed):
     """The split pass's runs and the merge's pieces, in their own arithmetic: every tile falls to one run, a CTA writes at most
     one partial result to each of its two slots, and the merge reads exactly the slots that were written."""
     rng = np.random.default_rng(seed)
-    for _ in range(60):
+    for case in range(80):
         S, groups = int(rng.integers(1, 20)), int(rng.integers(1, 5))
-        first = np.concatenate([[0], np.cumsum(rng.integers(0, 30, S) * (rng.random(S) < 0.8))]).astype(int)
-        total = int(first[-1]) * groups
-        ctas = min(int(rng.integers(1, 60)), total)
-        seen, slots = set(), {}
+        n = (rng.integers(0, 300 if case % 2 else 30, S) * (rng.random(S) < 0.8)).astype(int)
+        tiles, live = int(n.sum()), int((n > 0).sum())
+        ctas = min(int(rng.integers(1, 60)), tiles * groups)
+        extra = min(3, tiles * groups // (8 * ctas)) if ctas else 0
+        first = np.concatenate([[0], np.cumsum(n + extra * (n > 0))]).astype(int)
+        total = (tiles + extra * live) * groups
         each, more = divmod(total, ctas) if ctas else (0, 0)
 
         def begin(c):
@@ -307,6 +309,7 @@ def test_decode_share_out(seed):
             cut = more * (each + 1)
             return t // (each + 1) if t < cut else more + (t - cut) // each
 
+        seen, slots = set(), {}
         for c in range(ctas):
             at, end = begin(c), begin(c + 1)
             assert at < end
@@ -315,25 +318,25 @@ def test_decode_share_out(seed):
                 while hi - lo > 1:
                     mid = (lo + hi) // 2
                     lo, hi = (mid, hi) if first[mid] * groups <= at else (lo, mid)
-                n = int(first[lo + 1] - first[lo])
-                assert n > 0
-                hg, a = divmod(at - int(first[lo]) * groups, n)
-                b = min(n, a + end - at)
+                units = int(first[lo + 1] - first[lo])
+                assert units > extra
+                hg, u = divmod(at - int(first[lo]) * groups, units)
+                v = min(units, u + end - at)
+                at += v - u
+                a, b = max(u - extra, 0), max(v - extra, 0)
                 for t in range(a, b):
                     assert (lo, hg, t) not in seen
                     seen.add((lo, hg, t))
-                if not (a == 0 and b == n):
+                if a < b and not (a == 0 and b == units - extra):
                     slot = 2 * c + (1 if a == 0 else 0)
                     assert slot not in slots
                     slots[slot] = (lo, hg)
-                at += b - a
-        assert len(seen) == total
+        assert len(seen) == tiles * groups
         read = {}
         for s in range(S):
-            n = int(first[s + 1] - first[s])
-            for hg in range(groups if n else 0):
-                at = int(first[s]) * groups + hg * n
-                c0, c1 = owner(at), owner(at + n - 1)
+            for hg in range(groups if n[s] else 0):
+                at = int(first[s]) * groups + hg * int(n[s] + extra) + extra
+                c0, c1 = owner(at), owner(at + int(n[s]) - 1)
                 if c1 > c0:
                     read.update({2 * (c0 + i) + (1 if i == 0 else 0): (s, hg) for i in range(c1 - c0 + 1)})
         assert read == slots
