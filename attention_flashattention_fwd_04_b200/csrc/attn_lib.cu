@@ -83,18 +83,21 @@ int validate_cache8(const void* k_pool, const void* v_pool, const void* kv_scale
 // Launches a kernel that may begin while the one before it ends
 // (griddep_wait in rope.cuh).
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, cudaStream_t stream,
-                         const Args&... args) {
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned grid_y, unsigned threads, size_t smem, int cluster,
+                         cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid_x, grid_y);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -117,14 +120,14 @@ int launch_append8(const attn::RopeTable& table, attn::Append8Params p, bool rop
     p.tokens_log2 = row_tokens_log2(p.total_q);
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.total_q) + (1 << p.tokens_log2) - 1) >> p.tokens_log2);
     p.one_wave = grid <= static_cast<unsigned>(sms);
-    e = launch_early(attn::rope_append8_kernel<D>, grid, 1, attn::kRowThreads, 0, stream, table, p);
+    e = launch_early(attn::rope_append8_kernel<D>, grid, 1, attn::kRowThreads, 0, 1, stream, table, p);
   } else {
     // A warp an item, up to a few times what the SMs hold at once.
     constexpr int heads = 512 / D * attn::kAppend8Heads, warps = attn::kAppend8Threads / 32;
     const long long items = static_cast<long long>(p.total_q) * ((p.Hkv + heads - 1) / heads);
     const unsigned grid = static_cast<unsigned>(std::min<long long>((items + warps - 1) / warps, 16LL * sms));
     p.one_wave = grid <= static_cast<unsigned>(sms);
-    e = launch_early(attn::append8_kernel<D>, grid, 1, attn::kAppend8Threads, 0, stream, p);
+    e = launch_early(attn::append8_kernel<D>, grid, 1, attn::kAppend8Threads, 0, 1, stream, p);
   }
   if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
@@ -178,7 +181,8 @@ int append8(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, 
 // heads a tile covers and the room for partial results.
 struct Decode8Plan {
   int hb = 0;    // KV heads of a tile
-  int ctas = 0;  // CTAs of the split pass
+  int ctas = 0;  // CTAs of the split pass, or of a cluster
+  bool cluster = false;
   int box = 0;   // tokens of one TMA box
   size_t lse_offset = 0, total = 0;
 };
@@ -188,9 +192,24 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   const long long max_tokens = static_cast<long long>(max_pages) * page_size;
   if (max_tokens > INT_MAX) return false;
   Decode8Plan pl;
-  pl.hb = decode_heads_per_cta(Hkv);
   const int group = Hq / Hkv;
+  // Clusters, where one a sequence and KV head fills no more than the SMs hold
+  // (256 CTAs in clusters of up to 8; half with one CTA an SM) and a CTA has at
+  // most 4 tiles: no partial results and no second launch.
+  const long long heads = static_cast<long long>(num_seqs) * Hkv, head_tiles = (max_tokens + attn::kDecode8Rows - 1) / attn::kDecode8Rows;
+  const long long room = group <= 8 || d == 64 ? 256 : 128;
+  int most = 8;
+  while (most > 1 && (heads * most > room || most / 2 >= head_tiles)) most /= 2;
+  pl.cluster = heads * most <= room && head_tiles <= 4 * most;
+  pl.hb = pl.cluster ? 1 : decode_heads_per_cta(Hkv);
   const int tokens = attn::kDecode8Rows / pl.hb;
+  if (pl.cluster) {
+    pl.ctas = most;
+    pl.box = 16;
+    while (pl.box < tokens && page_size % (2 * pl.box) == 0) pl.box *= 2;
+    *out = pl;
+    return true;
+  }
   for (pl.box = 16; pl.box < tokens && page_size % (2 * pl.box) == 0;) pl.box *= 2;
   const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
   if (tiles + 3LL * attn::kDecode8MaxSeqs * (Hkv / pl.hb) > INT_MAX) return false;  // units of work, in 32 bits
@@ -218,20 +237,30 @@ bool encode_3d_bytes(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1
 }
 
 template <int D, int NT, int PER_SM, int STAGES>
-int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Decode8Params& p, cudaStream_t stream) {
+int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Decode8Params& p, bool cluster, cudaStream_t stream) {
   using L = attn::Decode8Layout<D, STAGES>;
-  auto kernel = attn::decode8_split_kernel<D, NT, PER_SM, STAGES>;
-  cudaError_t e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, PER_SM, STAGES>>(L::kAlloc);
+  cudaError_t e;
+  if (cluster) {
+    e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, PER_SM, STAGES, true>>(L::kAlloc);
+    if (e != cudaSuccess) return fail_cuda(e);
+    e = launch_early(attn::decode8_split_kernel<D, NT, PER_SM, STAGES, true>, static_cast<unsigned>(p.S * p.Hkv * p.ctas), 1, L::kThreads,
+                     L::kAlloc, p.ctas, stream, tk, tv, p);
+    if (e != cudaSuccess) return fail_cuda(e);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
+  }
+  e = ensure_smem_limit<attn::decode8_split_kernel<D, NT, PER_SM, STAGES, false>>(L::kAlloc);
   if (e != cudaSuccess) return fail_cuda(e);
-  e = launch_early(kernel, static_cast<unsigned>(p.ctas), 1, L::kThreads, L::kAlloc, stream, tk, tv, p);
+  e = launch_early(attn::decode8_split_kernel<D, NT, PER_SM, STAGES, false>, static_cast<unsigned>(p.ctas), 1, L::kThreads, L::kAlloc, 1,
+                   stream, tk, tv, p);
   if (e != cudaSuccess) return fail_cuda(e);
   // With few sequences and heads there are many partial rows for each: 16
   // warps share a head's, else one warp takes them.
   const bool wide = p.ctas > 16LL * p.S * (p.Hkv / p.hb);
   const int heads = wide ? 1 : attn::kMerge8Warps;
   const unsigned gx = static_cast<unsigned>((p.Hq + heads - 1) / heads), gy = static_cast<unsigned>(p.S);
-  e = wide ? launch_early(attn::decode8_merge_kernel<D, 16>, gx, gy, 32 * attn::kMerge8Warps, 0, stream, p)
-           : launch_early(attn::decode8_merge_kernel<D, 1>, gx, gy, 32 * attn::kMerge8Warps, 0, stream, p);
+  e = wide ? launch_early(attn::decode8_merge_kernel<D, 16>, gx, gy, 32 * attn::kMerge8Warps, 0, 1, stream, p)
+           : launch_early(attn::decode8_merge_kernel<D, 1>, gx, gy, 32 * attn::kMerge8Warps, 0, 1, stream, p);
   if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);
@@ -352,7 +381,7 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
   if (st == ATTN_ERR_UNSUPPORTED || Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
   Decode8Plan pl;
   if (!decode8_plan(num_seqs, Hq, Hkv, d, max_pages, page_size, &pl)) return ATTN_ERR_SHAPE;
-  if (!workspace || workspace_bytes < pl.total) return ATTN_ERR_WORKSPACE;
+  if (pl.total > 0 && (!workspace || workspace_bytes < pl.total)) return ATTN_ERR_WORKSPACE;
   if (st == ATTN_ERR_ALIGN || misaligned16(q) || misaligned16(o) || misaligned16(workspace) || misaligned4(lse))
     return ATTN_ERR_ALIGN;
 
@@ -394,9 +423,9 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
     // Two CTAs an SM, but one where 16 query heads of d = 128 need its registers.
     int rc;
     if (d == 128)
-      rc = p.group <= 8 ? launch_decode8<128, 1, 2, 3>(tk, tv, p, s) : launch_decode8<128, 2, 1, 6>(tk, tv, p, s);
+      rc = p.group <= 8 ? launch_decode8<128, 1, 2, 3>(tk, tv, p, pl.cluster, s) : launch_decode8<128, 2, 1, 6>(tk, tv, p, pl.cluster, s);
     else
-      rc = p.group <= 8 ? launch_decode8<64, 1, 2, 6>(tk, tv, p, s) : launch_decode8<64, 2, 2, 6>(tk, tv, p, s);
+      rc = p.group <= 8 ? launch_decode8<64, 1, 2, 6>(tk, tv, p, pl.cluster, s) : launch_decode8<64, 2, 2, 6>(tk, tv, p, pl.cluster, s);
     if (rc != ATTN_OK) return rc;
   }
   return ATTN_OK;

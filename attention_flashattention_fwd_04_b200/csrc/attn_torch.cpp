@@ -269,13 +269,16 @@ std::tuple<int, Tensor, Tensor> decode(const Tensor& q, const Tensor& k_pool, co
   on.add(o, "out");
   on.add(lse, "lse");
   const Call call(on);
-  const size_t need = workspace ? 0 : abi.decode_bytes(c.S, Hq, c.Hkv, c.d, c.max_pages, c.page_size);
-  const Tensor ws = workspace ? *workspace : at::empty({std::max<int64_t>(need, 16)}, q.options().dtype(at::kByte));
+  Maybe ws = workspace;
+  if (!ws) {
+    const size_t need = abi.decode_bytes(c.S, Hq, c.Hkv, c.d, c.max_pages, c.page_size);
+    if (need > 0) ws = at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte));
+  }
   Tensor oo = made(o, q.sizes(), q, at::kBFloat16), ol = made(lse, {c.S, Hq}, q, at::kFloat);
   const float s = scale ? static_cast<float>(*scale) : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.d)));
   const int rc = abi.decode(in(q), bytes(k_pool), bytes(v_pool), bytes(kv_scales), ints(block_table), ints(seq_lens), c.page_size, out(oo),
-                            static_cast<float*>(ol.data_ptr()), c.S, Hq, c.Hkv, c.d, c.max_pages, c.num_pages, s, ws.data_ptr(),
-                            ws.nbytes(), call.stream);
+                            static_cast<float*>(ol.data_ptr()), c.S, Hq, c.Hkv, c.d, c.max_pages, c.num_pages, s, ws ? ws->data_ptr() : nullptr,
+                            ws ? ws->nbytes() : 0, call.stream);
   return {rc, oo, ol};
 }
 

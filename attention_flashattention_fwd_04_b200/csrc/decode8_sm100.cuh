@@ -13,6 +13,10 @@
 // tiles writes its output; others write partial results, at most two a CTA,
 // which decode8_merge_kernel joins.
 //
+// Few and short sequences go without the merge: a cluster of up to 8 CTAs has one
+// sequence and KV head, and joins its results through its CTAs' shared memory
+// (one sequence of 1000 tokens: XONEX us against 8.1, and one launch less).
+//
 // A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
 // each of the 8 consumer warps works on 16 of the tile's rows, 16 tokens of one
 // KV head, for 8 NT of its query heads.  Both products run on mma.sync m16n8k16
@@ -68,7 +72,8 @@ struct Decode8Layout {
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
   static constexpr int kJoin = kWarpSums + 2 * kWarps * 4;    // bounds and sums of the warps, [2][warp][16 heads]
   static constexpr int kTiles = kJoin + 2 * kWarps * 16 * 4;
-  static constexpr int kBytes = kTiles + (kDecode8MaxSeqs + 1) * 4;
+  static constexpr int kOwn = kTiles;                    // of a cluster's CTA instead: its result, 16 rows of D floats
+  static constexpr int kBytes = kTiles + (16 * D > kDecode8MaxSeqs + 1 ? 16 * D : kDecode8MaxSeqs + 1) * 4;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -158,6 +163,7 @@ __device__ __forceinline__ int decode8_count(int len, int log2) { return (len >>
 // c of n takes total / n units, and one more if c < total % n.
 struct Decode8Share {
   int extra, groups, ctas, each, more;
+  Decode8Share() = default;
   // tiles, sequences: of one head group, all and those with tokens.
   __device__ __forceinline__ Decode8Share(int tiles, int sequences, int groups, int most) : groups(groups) {
     ctas = min(most, tiles * groups);
@@ -203,6 +209,32 @@ __device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, c
   r.from = max(in - share.extra, 0);
   r.to = max(to - share.extra, 0);
   return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// `addr` of this CTA's shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
 }
 
 // One tile for one warp.
@@ -364,8 +396,10 @@ struct Decode8Warp {
   }
 };
 
-// NT tiles of 8 query heads a KV head.  PER_SM: CTAs an SM.
-template <int D, int NT, int PER_SM, int STAGES>
+// NT tiles of 8 query heads a KV head.  PER_SM: CTAs an SM.  CLUSTER: p.ctas CTAs,
+// a cluster, share the tiles of one sequence and KV head (hb = 1); else p.ctas
+// share all there are.
+template <int D, int NT, int PER_SM, int STAGES, bool CLUSTER>
 __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     decode8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const Decode8Params p) {
@@ -396,64 +430,100 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   // this grid): not earlier, so that what it reads is behind those kernels too.
   griddep_launch();
 
-  // Units before each sequence: every consumer thread sums up tiles and
-  // sequences of a run of lengths, the warps' sums follow.
-  const int per = (p.S + 32 * kDecode8Warps - 1) / (32 * kDecode8Warps);
-  int tiles = 0, count = 0;  // of this thread's run; then of all before it
-  if (warp < kDecode8Warps) {
-    for (int i = 0; i < per; ++i) {
-      const int s = threadIdx.x * per + i;
-      if (s >= p.S) break;
-      int len = p.seq_lens[s];
-      if (len < 0 || len > p.max_pages * p.page_size) {
-        if (blockIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
-        len = 0;
+  int begin = 0, end = 0;
+  Decode8Share share;
+  Decode8Run mine;  // of a cluster's CTA
+  int rank = 0, active = 0;
+  if constexpr (CLUSTER) {
+    const int index = blockIdx.x / p.ctas;
+    rank = blockIdx.x - index * p.ctas;
+    mine.s = index / p.Hkv;
+    mine.hg = index - mine.s * p.Hkv;
+    const int len = p.seq_lens[mine.s];
+    const size_t head = static_cast<size_t>(mine.s) * p.Hq + mine.hg * p.group;
+    if (len <= 0 || len > p.max_pages * p.page_size) {
+      if (rank == 0) {
+        if (threadIdx.x == 0 && mine.hg == 0 && len != 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+        for (int i = threadIdx.x; i < p.group * (D / 8); i += L::kThreads)
+          reinterpret_cast<uint4*>(p.o + head * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = threadIdx.x; i < p.group; i += L::kThreads) p.lse[head + i] = -INFINITY;
       }
-      first[s + 1] = decode8_count(len, tokens_log2);
-      tiles += first[s + 1];
-      count += len > 0;
+      return;  // all of the cluster
     }
-    const int own_tiles = tiles, own_count = count;
+    mine.n = decode8_count(len, tokens_log2);
+    active = min(p.ctas, mine.n);
+    const int each = mine.n / active, more = mine.n - each * active;
+    mine.from = min(rank, active) * each + min(rank, more);
+    mine.to = mine.from + (rank < active ? each + (rank < more) : 0);
+    mine.next = end = 1;
+    __syncthreads();  // the barriers are set up
+  }
+
+  if constexpr (!CLUSTER) {
+    // Units before each sequence: every consumer thread sums up tiles and
+    // sequences of a run of lengths, the warps' sums follow.
+    const int per = (p.S + 32 * kDecode8Warps - 1) / (32 * kDecode8Warps);
+    int tiles = 0, count = 0;  // of this thread's run; then of all before it
+    if (warp < kDecode8Warps) {
+      for (int i = 0; i < per; ++i) {
+        const int s = threadIdx.x * per + i;
+        if (s >= p.S) break;
+        int len = p.seq_lens[s];
+        if (len < 0 || len > p.max_pages * p.page_size) {
+          if (blockIdx.x == 0) atomicOr(&g_attn_device_error, kErrCache8Table);
+          len = 0;
+        }
+        first[s + 1] = decode8_count(len, tokens_log2);
+        tiles += first[s + 1];
+        count += len > 0;
+      }
+      const int own_tiles = tiles, own_count = count;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, tiles, off), y = __shfl_up_sync(0xffffffffu, count, off);
-      if (lane >= off) {
-        tiles += x;
-        count += y;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, tiles, off), y = __shfl_up_sync(0xffffffffu, count, off);
+        if (lane >= off) {
+          tiles += x;
+          count += y;
+        }
+      }
+      if (lane == 31) {
+        warp_sums[warp] = tiles;
+        warp_sums[kDecode8Warps + warp] = count;
+      }
+      tiles -= own_tiles;
+      count -= own_count;
+    }
+    if (threadIdx.x == 0) first[0] = 0;
+    __syncthreads();
+    int all_tiles = 0, all_count = 0;
+#pragma unroll
+    for (int w = 0; w < kDecode8Warps; ++w) {
+      if (w == warp) {
+        tiles += all_tiles;
+        count += all_count;
+      }
+      all_tiles += warp_sums[w];
+      all_count += warp_sums[kDecode8Warps + w];
+    }
+    share = Decode8Share(all_tiles, all_count, p.Hkv >> p.hb_log2, p.ctas);
+    if (warp < kDecode8Warps) {
+      for (int i = 0; i < per; ++i) {
+        const int s = threadIdx.x * per + i;
+        if (s >= p.S) break;
+        tiles += first[s + 1];
+        count += first[s + 1] > 0;
+        first[s + 1] = share.units(tiles, count);
       }
     }
-    if (lane == 31) {
-      warp_sums[warp] = tiles;
-      warp_sums[kDecode8Warps + warp] = count;
-    }
-    tiles -= own_tiles;
-    count -= own_count;
+    __syncthreads();
+    if (static_cast<int>(blockIdx.x) >= share.ctas) return;
+    begin = share.begin(blockIdx.x);
+    end = share.begin(blockIdx.x + 1);
   }
-  if (threadIdx.x == 0) first[0] = 0;
-  __syncthreads();
-  int all_tiles = 0, all_count = 0;
-#pragma unroll
-  for (int w = 0; w < kDecode8Warps; ++w) {
-    if (w == warp) {
-      tiles += all_tiles;
-      count += all_count;
-    }
-    all_tiles += warp_sums[w];
-    all_count += warp_sums[kDecode8Warps + w];
-  }
-  const Decode8Share share(all_tiles, all_count, p.Hkv >> p.hb_log2, p.ctas);
-  if (warp < kDecode8Warps) {
-    for (int i = 0; i < per; ++i) {
-      const int s = threadIdx.x * per + i;
-      if (s >= p.S) break;
-      tiles += first[s + 1];
-      count += first[s + 1] > 0;
-      first[s + 1] = share.units(tiles, count);
-    }
-  }
-  __syncthreads();
-  if (static_cast<int>(blockIdx.x) >= share.ctas) return;
-  const int begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
+  auto run_at = [&](int at) {
+    if constexpr (CLUSTER) return mine;
+    else return decode8_run(first, p.S, share, at, end);
+  };
 
   if (warp == kDecode8Warps) {
     // ------------------------------------------------------------ producer
@@ -469,7 +539,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     uint32_t phase = 1;     // of the empty barriers: the ring's first round finds every place free
     const int page_chunks = p.page_size / 16;
     for (int at = begin; at < end && ok;) {
-      const Decode8Run run = decode8_run(first, p.S, share, at, end);
+      const Decode8Run run = run_at(at);
       at = run.next;
       if (run.from == run.to) continue;
       const int len = p.seq_lens[run.s];
@@ -537,6 +607,11 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     // No copy may be in flight when the CTA ends.
     for (int c = max(0, count - STAGES); c < count; ++c)
       mbar_wait(full_bar(c % STAGES), static_cast<uint32_t>(c / STAGES) & 1u, kErrCache8Wait);
+    __syncwarp();
+    if constexpr (CLUSTER) {
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -550,7 +625,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
   for (int at = begin; at < end;) {
-    const Decode8Run run = decode8_run(first, p.S, share, at, end);
+    const Decode8Run run = run_at(at);
     at = run.next;
     if (run.from == run.to) continue;
     const int len = p.seq_lens[run.s];
@@ -633,7 +708,9 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       for (int i = 0; i < parts; ++i)
         join[i * p.hb * 16 + at_head] = ex2_approx(join[i * p.hb * 16 + at_head] - mx - 6.f) / sum;
       const float lse2 = mx + log2f(sum);
-      if (whole)
+      if (CLUSTER)
+        join[kDecode8Warps * 16 + threadIdx.x] = lse2;  // (in the place of this head's first sum)
+      else if (whole)
         p.lse[head0 + threadIdx.x] = lse2 * 0.69314718055994530942f;
       else
         p.part_lse[row0 + threadIdx.x] = lse2;
@@ -653,10 +730,10 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
 #pragma unroll
         for (int u = 0; u < 8; ++u) x[u] = fmaf(a, src[(from * (D / 4) + k) * 32 + ((4 * u + t) ^ k)], x[u]);
       }
-      if (whole) {
+      if (!CLUSTER && whole) {
         *reinterpret_cast<uint4*>(p.o + (head0 + row) * D + 8 * octet) = pack_bf16x8(x);
       } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (row0 + row) * D + 8 * octet);
+        float4* dst = reinterpret_cast<float4*>(CLUSTER ? reinterpret_cast<float*>(smem + L::kOwn) + row * D + 8 * octet : p.part_o + (row0 + row) * D + 8 * octet);
         dst[0] = make_float4(x[0], x[1], x[2], x[3]);
         dst[1] = make_float4(x[4], x[5], x[6], x[7]);
       }
@@ -667,6 +744,53 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mbar_arrive(empty_bar(place[nt]));
     }
+  }
+  if constexpr (CLUSTER) {
+    // The cluster's CTAs join their results, each for a share of the values.
+    __syncwarp();
+    cluster_sync();
+    const size_t head = static_cast<size_t>(mine.s) * p.Hq + mine.hg * p.group;
+    for (int i = threadIdx.x * p.ctas + rank; i < p.group * (D / 8); i += 32 * kDecode8Warps * p.ctas) {
+      const int row = i / (D / 8), octet = i % (D / 8);
+      const uint32_t own = base + L::kOwn + (row * D + 8 * octet) * 4, own_lse = base + L::kJoin + (kDecode8Warps * 16 + row) * 4;
+      float l[8], top = -INFINITY, sum = 0.f, x[8];
+      float4 a[8], b[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        l[c] = -INFINITY;
+        if (c < active) {
+          l[c] = cluster_load(cluster_map(own_lse, c));
+          a[c] = cluster_load4(cluster_map(own, c));
+          b[c] = cluster_load4(cluster_map(own + 16, c));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) top = fmaxf(top, l[c]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c < active) {
+          const float w = ex2_approx(l[c] - top);
+          sum += w;
+          x[0] = fmaf(w, a[c].x, x[0]);
+          x[1] = fmaf(w, a[c].y, x[1]);
+          x[2] = fmaf(w, a[c].z, x[2]);
+          x[3] = fmaf(w, a[c].w, x[3]);
+          x[4] = fmaf(w, b[c].x, x[4]);
+          x[5] = fmaf(w, b[c].y, x[5]);
+          x[6] = fmaf(w, b[c].z, x[6]);
+          x[7] = fmaf(w, b[c].w, x[7]);
+        }
+      }
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] *= inv;
+      *reinterpret_cast<uint4*>(p.o + (head + row) * D + 8 * octet) = pack_bf16x8(x);
+      if (octet == 0) p.lse[head + row] = (top + log2f(sum)) * 0.69314718055994530942f;
+    }
+    __syncwarp();
+    cluster_sync();  // nobody leaves while others read its shared memory
   }
 }
 

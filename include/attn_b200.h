@@ -464,7 +464,8 @@ int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint
  * are fp32.  Slots past seq_len, their scales too, may hold anything.
  * The workspace's contents do not matter; calls that can overlap need one each,
  * captured graphs that can be replayed at the same time among them.
- * paged_attn_decode_fp8_workspace_bytes: its size (0 for invalid sizes).
+ * paged_attn_decode_fp8_workspace_bytes: its size; 0 for invalid sizes, and for
+ * few and short sequences, which need none (workspace may then be NULL).
  */
 size_t paged_attn_decode_fp8_workspace_bytes(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_size);
 int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales,

@@ -200,7 +200,7 @@ def test_8bit_cache_calls_reject(lib, fn, kw, code):
     ("gather", dict(ko=None), 1), ("gather", dict(vo=None), 1), ("gather", dict(ko=FAKE + 8), 3), ("gather", dict(vo=FAKE + 16), 3),
     ("decode", dict(q=None), 1), ("decode", dict(o=None), 1), ("decode", dict(lse=None), 1), ("decode", dict(Hq=7), 2),
     ("decode", dict(scale=0.0), 2), ("decode", dict(scale=math.nan), 2), ("decode", dict(Hq=34), 5),
-    ("decode", dict(ws=None), 4), ("decode", dict(wb=16), 4), ("decode", dict(ws=FAKE + 8), 3), ("decode", dict(q=FAKE + 2), 3),
+    ("decode", dict(ws=None, mp=512), 4), ("decode", dict(wb=16, mp=512), 4), ("decode", dict(ws=FAKE + 8, mp=512), 3), ("decode", dict(q=FAKE + 2), 3),
     ("decode", dict(lse=FAKE + 2), 3),
 ])
 def test_8bit_cache_calls_reject_their_own(lib, fn, kw, code):
@@ -214,7 +214,8 @@ def test_8bit_cache_calls_with_no_rows_are_no_ops(lib, fn):
 
 def test_decode_fp8_workspace(lib):
     w = lib.paged_attn_decode_fp8_workspace_bytes
-    assert w(4, 32, 8, 128, 64, 16) > 0 and w(4, 32, 8, 128, 64, 16) % 4 == 0
+    assert w(64, 32, 8, 128, 512, 16) > 0 and w(64, 32, 8, 128, 512, 16) % 16 == 0
+    assert w(4, 32, 8, 128, 64, 16) == 0  # few and short sequences need none
     assert w(0, 32, 8, 128, 64, 16) == 0 and w(4, 32, 8, 96, 64, 16) == 0 and w(4, 32, 0, 128, 64, 16) == 0
 
 

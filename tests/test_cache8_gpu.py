@@ -383,12 +383,24 @@ DECODES = [
     (16, 1, 64, 64, [63, 64, 65, 1500]), (12, 3, 128, 48, [513, 2, 0, 2100]), (4, 2, 64, 16, [16, 48, 80, 777]),
     (64, 4, 128, 256, [255, 3000]), (7, 1, 128, 16, [129]), (9, 1, 64, 16, [40, 1]), (10, 10, 64, 16, [70]),
     (24, 6, 128, 128, [5, 333]), (2, 1, 128, 16, [20000]), (32, 2, 64, 64, [9000, 4097]),
+    (16, 1, 128, 32, [4096, 0, 3000, 129]), (32, 4, 64, 16, [500, 128, 127]), (8, 8, 128, 16, [1, 100] * 16),
 ]
 
 
+def widen(c, tokens=8192):
+    """A table for longer sequences (room for `tokens`): the calls that do not fit a cluster's CTAs, by the sizes alone."""
+    S, width = c["table"].shape
+    room = -(-tokens // c["ps"])
+    c["table"] = torch.cat([c["table"], torch.full((S, max(0, room - width)), -1, dtype=torch.int32)], 1).contiguous()
+    return c
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("Hq,Hkv,d,ps,lens", DECODES)
-def test_decode(Hq, Hkv, d, ps, lens):
+def test_decode(Hq, Hkv, d, ps, lens, wide):
     c = filled_case(40, lens, Hkv, d, ps)
+    if wide:
+        widen(c)
     q = rows(41, len(lens), Hq, d)
     scale = float(np.float32(d ** -0.5))
     o, lse = run_decode(c, q, scale)
@@ -396,8 +408,9 @@ def test_decode(Hq, Hkv, d, ps, lens):
     assert_decoded(c, q, scale, o, lse)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("t_star", [0, 15, 16, 63, 64, 255, 256, 999, 1000])
-def test_decode_reads_the_right_slot(t_star):
+def test_decode_reads_the_right_slot(t_star, wide):
     """One token outweighs all others: O is its value row, bit for bit."""
     L, Hkv, d, ps = 1001, 2, 128, 16
     c = cache_case(42, [0, 0], [L, 37], Hkv, d, ps)
@@ -408,14 +421,15 @@ def test_decode_reads_the_right_slot(t_star):
     c["kp"], c["vp"], c["sc"] = (torch.from_numpy(np.ascontiguousarray(a)) for a in (wk, wv, ws))
     q = torch.zeros(2, 8, d)
     q[..., 0] = 1.0
-    o, lse = run_decode(c, q.to(torch.bfloat16), 0.125)
+    o, lse = run_decode(widen(c) if wide else c, q.to(torch.bfloat16), 0.125)
     page, slot = int(c["table"][0, t_star // ps]), t_star % ps
     want = oracle.dequantise(wv[page, slot], ws[page, :, slot, 1])
     assert np.array_equal(f64(o)[0], np.repeat(want, 4, axis=0))
     assert np.allclose(f64(lse)[0], 256.0, atol=2.0 ** -12)
 
 
-def test_decode_scales_far_apart():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_scales_far_apart(wide):
     """Values whose scales span the whole range: the largest must not drown the weights of the others, nor overflow."""
     d, ps, L = 64, 16, 96
     for seed, (lo, hi) in enumerate([(-90, 110), (-60, 60), (-100, -80), (90, 119)]):
@@ -430,6 +444,8 @@ def test_decode_scales_far_apart():
         wk, wv, ws = oracle_append(c)
         c["kp"], c["vp"], c["sc"] = (torch.from_numpy(np.ascontiguousarray(a)) for a in (wk, wv, ws))
         q = rows(60 + seed, 1, 4, d)
+        if wide:
+            widen(c)
         o, lse = run_decode(c, q, 0.125)
         assert_decoded(c, q, 0.125, o, lse)
 
@@ -444,8 +460,11 @@ def test_decode_queries_of_any_size(size):
     assert_decoded(c, q, scale, o, lse)
 
 
-def test_decode_reports_bad_input_and_goes_on():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_reports_bad_input_and_goes_on(wide):
     c = filled_case(72, [100, 50, 30, 20], 2, 128, 16)
+    if wide:
+        widen(c)
     q = rows(73, 4, 8, 128)
     good, good_lse = run_decode(c, q, 0.1)
     assert api.device_status() == 0
@@ -458,10 +477,11 @@ def test_decode_reports_bad_input_and_goes_on():
 
 
 def test_decode_garbage_workspace_shared_pages_and_repeat():
-    c = filled_case(74, [400, 390, 64], 2, 128, 16)
+    c = widen(filled_case(74, [400, 390, 64], 2, 128, 16))
     c["table"][1, :20], c["table"][2, :4] = c["table"][0, :20].clone(), c["table"][0, :4].clone()
     q = rows(75, 3, 8, 128)
     need = api.paged_attn_decode_fp8_workspace_bytes(3, 8, 2, 128, c["table"].shape[1], 16)
+    assert need > 0
     ws = torch.full((need // 4 + 1,), float("nan"), device="cuda")
     o, lse = run_decode(c, q, 0.1, workspace=ws)
     assert_decoded(c, q, 0.1, o, lse)
@@ -469,11 +489,14 @@ def test_decode_garbage_workspace_shared_pages_and_repeat():
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])  # the same sums in the same order
 
 
-def test_decode_empty_batch_and_single_token():
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_empty_batch_and_single_token(wide):
     c = filled_case(76, [0, 0, 0], 2, 64, 16)
+    if wide:
+        widen(c)
     o, lse = run_decode(c, rows(77, 3, 4, 64), 0.1)
     assert api.device_status() == 0 and not o.any() and torch.all(lse == -float("inf"))
-    c = filled_case(78, [1], 1, 64, 16)  # one token: its value row, and its score
+    c = widen(filled_case(78, [1], 1, 64, 16), 8192 if wide else 16)  # one token: its value row, and its score
     q = rows(79, 1, 1, 64)
     o, lse = run_decode(c, q, 0.1)
     page = int(c["table"][0, 0])
@@ -594,7 +617,7 @@ def test_serving_steps_together():
 
 def test_calls_on_another_stream():
     """Everything a call makes for itself lives on the stream it runs on."""
-    c = filled_case(84, [3000, 2500], 2, 128, 16)
+    c = widen(filled_case(84, [3000, 2500], 2, 128, 16))
     q = rows(85, 2, 8, 128)
     want = run_decode(c, q, 0.1)
     kp, vp, sc = gpu_cache(c)
@@ -615,10 +638,11 @@ def test_calls_on_another_stream():
     assert torch.equal(qo, qc)
 
 
-def test_steps_back_to_back_equal_steps_apart():
+@pytest.mark.parametrize("short", [False, True])
+def test_steps_back_to_back_equal_steps_apart(short):
     """A chain of steps whose kernels may begin while the ones before them end gives, bit for bit, what the same steps give with
     the device idle between them."""
-    S, Hq, Hkv, d, ps, width = 5, 16, 4, 128, 16, 40
+    S, Hq, Hkv, d, ps, width = 5, 16, 4, 128, 16, 40 if short else 400
     spec = make_spec(d)
     table = torch.randperm(S * width, generator=torch.Generator().manual_seed(120)).to(torch.int32).view(S, width).cuda()
     one = torch.arange(S + 1, dtype=torch.int32).cuda()
@@ -648,7 +672,7 @@ def test_steps_back_to_back_equal_steps_apart():
 
 
 def test_two_graphs_of_one_memory_pool_and_two_streams():
-    c, c2 = filled_case(140, [700, 33], 2, 128, 16), filled_case(141, [5, 900], 2, 128, 16)
+    c, c2 = widen(filled_case(140, [700, 33], 2, 128, 16)), widen(filled_case(141, [5, 900], 2, 128, 16))
     args = []
     for x, seed in ((c, 142), (c2, 143)):
         kp, vp, sc = gpu_cache(x)
