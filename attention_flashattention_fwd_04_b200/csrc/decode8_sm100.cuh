@@ -15,7 +15,7 @@
 //
 // Few and short sequences go without the merge: a cluster of up to 8 CTAs has one
 // sequence and KV head, and joins its results through its CTAs' shared memory
-// (one sequence of 1000 tokens: XONEX us against 8.1, and one launch less).
+// (one sequence of 1000 tokens: 6.3 us against 8.1, and one launch less).
 //
 // A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
 // each of the 8 consumer warps works on 16 of the tile's rows, 16 tokens of one
@@ -72,8 +72,10 @@ struct Decode8Layout {
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
   static constexpr int kJoin = kWarpSums + 2 * kWarps * 4;    // bounds and sums of the warps, [2][warp][16 heads]
   static constexpr int kTiles = kJoin + 2 * kWarps * 16 * 4;
-  static constexpr int kOwn = kTiles;                    // of a cluster's CTA instead: its result, 16 rows of D floats
-  static constexpr int kBytes = kTiles + (16 * D > kDecode8MaxSeqs + 1 ? 16 * D : kDecode8MaxSeqs + 1) * 4;
+  // Of a cluster's CTA instead: its share of the values of all CTAs' results (16
+  // rows of D floats in all), and their LSEs [8][16].
+  static constexpr int kOwn = kTiles, kOwnLse = kOwn + 16 * D * 4;
+  static constexpr int kBytes = kTiles + (16 * D + 128 > kDecode8MaxSeqs + 1 ? 16 * D + 128 : kDecode8MaxSeqs + 1) * 4;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -211,9 +213,9 @@ __device__ __forceinline__ Decode8Run decode8_run(const int32_t* first, int S, c
   return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
+// The cluster's barrier: every thread arrives and waits in turn.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // `addr` of this CTA's shared memory in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
@@ -222,19 +224,12 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
   return a;
 }
 
-__device__ __forceinline__ float cluster_load(uint32_t addr) {
-  float x;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-  return x;
+__device__ __forceinline__ void cluster_store(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
-__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
-  float4 x;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(addr)
-               : "memory");
-  return x;
+__device__ __forceinline__ void cluster_store4(uint32_t addr, const float (&x)[4]) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
 }
 
 // One tile for one warp.
@@ -416,6 +411,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens_log2 = kDecode8RowsLog2 - p.hb_log2, tokens = 1 << tokens_log2;  // of a tile
 
+  if constexpr (CLUSTER) cluster_arrive();  // waited for before the first store to another CTA: it has begun by then
   if (threadIdx.x == 0) {
     for (int st = 0; st < STAGES; ++st) {
       mbar_init(full_bar(st), 1);
@@ -609,8 +605,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       mbar_wait(full_bar(c % STAGES), static_cast<uint32_t>(c / STAGES) & 1u, kErrCache8Wait);
     __syncwarp();
     if constexpr (CLUSTER) {
-      cluster_sync();
-      cluster_sync();
+      cluster_wait();
+      cluster_arrive();
     }
     return;
   }
@@ -698,42 +694,63 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     const size_t row0 = (2 * static_cast<size_t>(blockIdx.x) + (run.from == 0 ? 1 : 0)) * p.hb * p.group;
     const size_t head0 = static_cast<size_t>(run.s) * p.Hq + static_cast<size_t>(run.hg) * p.hb * p.group;
     const int heads = p.hb * p.group;  // rows of the result
-    if (static_cast<int>(threadIdx.x) < heads) {
-      const int g = threadIdx.x / p.group, at_head = g * 16 + threadIdx.x % p.group;
-      float mx = -INFINITY, sum = 0.f;
-      for (int i = 0; i < parts; ++i) mx = fmaxf(mx, join[i * p.hb * 16 + at_head]);
-      for (int i = 0; i < parts; ++i)
-        sum += join[(kDecode8Warps + i * p.hb) * 16 + at_head] * ex2_approx(join[i * p.hb * 16 + at_head] - mx);
-      // O = sum over the warps of acc * 2^(m - mx - 6) / sum
-      for (int i = 0; i < parts; ++i)
-        join[i * p.hb * 16 + at_head] = ex2_approx(join[i * p.hb * 16 + at_head] - mx - 6.f) / sum;
+    // A thread a head and warp that holds tokens of it: 8 times the group in all.
+    if (warp * 4 < p.group) {
+      const bool on = static_cast<int>(threadIdx.x) < 8 * p.group;  // the others of the last warp repeat its last
+      const int index = min(static_cast<int>(threadIdx.x), 8 * p.group - 1);
+      const int part = index & (parts - 1), row = index >> (3 - p.hb_log2);
+      const int g = row / p.group, mine_at = (part * p.hb + g) * 16 + row - g * p.group;
+      const float m = join[mine_at];
+      float mx = m;
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1)
+        if (off < parts) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      float sum = join[kDecode8Warps * 16 + mine_at] * ex2_approx(m - mx);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1)
+        if (off < parts) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      __syncwarp();
+      if (on) join[mine_at] = ex2_approx(m - mx - 6.f) / sum;  // O = sum over the warps of acc * 2^(m - mx - 6) / sum
       const float lse2 = mx + log2f(sum);
-      if (CLUSTER)
-        join[kDecode8Warps * 16 + threadIdx.x] = lse2;  // (in the place of this head's first sum)
-      else if (whole)
-        p.lse[head0 + threadIdx.x] = lse2 * 0.69314718055994530942f;
-      else
-        p.part_lse[row0 + threadIdx.x] = lse2;
+      if constexpr (CLUSTER) {
+        cluster_wait();  // (these warps here, the others below)
+        // Every CTA of the cluster gets this one's: threads 8 a head, a CTA each.
+        if (on && part < p.ctas) cluster_store(cluster_map(base + L::kOwnLse + (rank * 16 + row) * 4, part), lse2);
+      } else if (on && part == 0) {
+        if (whole)
+          p.lse[head0 + row] = lse2 * 0.69314718055994530942f;
+        else
+          p.part_lse[row0 + row] = lse2;
+      }
+    } else if constexpr (CLUSTER) {
+      cluster_wait();
     }
     decode8_consumers_sync<32 * kDecode8Warps>();
-    for (int i = threadIdx.x; i < heads * (D / 8); i += 32 * kDecode8Warps) {
-      const int row = i / (D / 8), octet = i % (D / 8);
-      const int g = row / p.group, h = row % p.group;
-      const int k = 2 * octet + (h & 1), t = (h & 7) >> 1;
+    // Values of a thread at a time: 4 in a cluster, whose CTAs have few heads, else 8.
+    constexpr int kValues = CLUSTER ? 4 : 8;
+    for (int i = threadIdx.x; i < heads * (D / kValues); i += 32 * kDecode8Warps) {
+      const int row = i / (D / kValues), set = i % (D / kValues);
+      const int g = row / p.group, h = row - g * p.group;
+      const int k = 2 * (set * kValues / 8) + (h & 1), t = (CLUSTER ? 16 * (set & 1) : 0) + ((h & 7) >> 1);
       const float* src = reinterpret_cast<const float*>(smem + (NT == 1 || h < 8 ? place[0] : place[NT - 1]) * L::kStage);
-      float x[8];
+      float x[kValues];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = 0.f;
+      for (int u = 0; u < kValues; ++u) x[u] = 0.f;
+#pragma unroll 2
       for (int part = 0; part < parts; ++part) {
         const int from = part * p.hb + g;
         const float a = join[from * 16 + h];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = fmaf(a, src[(from * (D / 4) + k) * 32 + ((4 * u + t) ^ k)], x[u]);
+        for (int u = 0; u < kValues; ++u) x[u] = fmaf(a, src[(from * (D / 4) + k) * 32 + ((4 * u + t) ^ k)], x[u]);
       }
-      if (!CLUSTER && whole) {
-        *reinterpret_cast<uint4*>(p.o + (head0 + row) * D + 8 * octet) = pack_bf16x8(x);
+      if constexpr (CLUSTER) {
+        // To the CTA that has this share of the values.
+        const int slot = (rank * 16 + row) * (D / 4 / p.ctas) + set / p.ctas;
+        cluster_store4(cluster_map(base + L::kOwn + slot * 16, set % p.ctas), x);
+      } else if (whole) {
+        *reinterpret_cast<uint4*>(p.o + (head0 + row) * D + 8 * set) = pack_bf16x8(x);
       } else {
-        float4* dst = reinterpret_cast<float4*>(CLUSTER ? reinterpret_cast<float*>(smem + L::kOwn) + row * D + 8 * octet : p.part_o + (row0 + row) * D + 8 * octet);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + (row0 + row) * D + 8 * set);
         dst[0] = make_float4(x[0], x[1], x[2], x[3]);
         dst[1] = make_float4(x[4], x[5], x[6], x[7]);
       }
@@ -746,51 +763,40 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     }
   }
   if constexpr (CLUSTER) {
-    // The cluster's CTAs join their results, each for a share of the values.
+    // All results of the cluster for this CTA's share of the values are joined.
     __syncwarp();
-    cluster_sync();
+    if (mine.from == mine.to) cluster_wait();  // (a CTA without tiles has not met the barrier's first round yet)
+    cluster_arrive();
+    cluster_wait();
     const size_t head = static_cast<size_t>(mine.s) * p.Hq + mine.hg * p.group;
-    for (int i = threadIdx.x * p.ctas + rank; i < p.group * (D / 8); i += 32 * kDecode8Warps * p.ctas) {
-      const int row = i / (D / 8), octet = i % (D / 8);
-      const uint32_t own = base + L::kOwn + (row * D + 8 * octet) * 4, own_lse = base + L::kJoin + (kDecode8Warps * 16 + row) * 4;
-      float l[8], top = -INFINITY, sum = 0.f, x[8];
-      float4 a[8], b[8];
+    const int quads = D / 4 / p.ctas;
+    for (int i = threadIdx.x; i < p.group * quads; i += 32 * kDecode8Warps) {
+      const int row = i / quads, slot = i - row * quads;
+      const float4* own = reinterpret_cast<const float4*>(smem + L::kOwn) + row * quads + slot;
+      const float* own_lse = reinterpret_cast<const float*>(smem + L::kOwnLse) + row;
+      float l[8], top = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      float4 a[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        l[c] = -INFINITY;
-        if (c < active) {
-          l[c] = cluster_load(cluster_map(own_lse, c));
-          a[c] = cluster_load4(cluster_map(own, c));
-          b[c] = cluster_load4(cluster_map(own + 16, c));
-        }
+        const bool there = c < active;
+        l[c] = there ? own_lse[c * 16] : -INFINITY;
+        a[c] = there ? own[c * 16 * quads] : make_float4(0.f, 0.f, 0.f, 0.f);
+        top = fmaxf(top, l[c]);
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) top = fmaxf(top, l[c]);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = 0.f;
-#pragma unroll
       for (int c = 0; c < 8; ++c) {
-        if (c < active) {
-          const float w = ex2_approx(l[c] - top);
-          sum += w;
-          x[0] = fmaf(w, a[c].x, x[0]);
-          x[1] = fmaf(w, a[c].y, x[1]);
-          x[2] = fmaf(w, a[c].z, x[2]);
-          x[3] = fmaf(w, a[c].w, x[3]);
-          x[4] = fmaf(w, b[c].x, x[4]);
-          x[5] = fmaf(w, b[c].y, x[5]);
-          x[6] = fmaf(w, b[c].z, x[6]);
-          x[7] = fmaf(w, b[c].w, x[7]);
-        }
+        const float w = ex2_approx(l[c] - top);
+        sum += w;
+        x[0] = fmaf(w, a[c].x, x[0]);
+        x[1] = fmaf(w, a[c].y, x[1]);
+        x[2] = fmaf(w, a[c].z, x[2]);
+        x[3] = fmaf(w, a[c].w, x[3]);
       }
       const float inv = 1.f / sum;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] *= inv;
-      *reinterpret_cast<uint4*>(p.o + (head + row) * D + 8 * octet) = pack_bf16x8(x);
-      if (octet == 0) p.lse[head + row] = (top + log2f(sum)) * 0.69314718055994530942f;
+      *reinterpret_cast<uint2*>(p.o + (head + row) * D + 4 * (slot * p.ctas + rank)) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+      if (slot == 0 && rank == 0) p.lse[head + row] = (top + log2f(sum)) * 0.69314718055994530942f;
     }
-    __syncwarp();
-    cluster_sync();  // nobody leaves while others read its shared memory
   }
 }
 
