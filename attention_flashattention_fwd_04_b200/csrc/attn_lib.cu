@@ -194,13 +194,24 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   Decode8Plan pl;
   const int group = Hq / Hkv;
   // Clusters, where one a sequence and KV head fills no more than the SMs hold
-  // (256 CTAs in clusters of up to 8; half with one CTA an SM) and a CTA has at
-  // most 4 tiles: no partial results and no second launch.
+  // and a CTA has few tiles: no partial results and no second launch, but no even
+  // shares either.  Up to 8 tiles where they fill half the SMs or more (16
+  // sequences of 2000 tokens, 8 KV heads: 17.5 us against 22.3; one of 2000 among
+  // 15 of 100: 12.8 against 12.5; with up to 16, one of 4000 among 15: 20.2 against
+  // 13.4), else 4 (one of 4000 tokens, 8 KV heads: 8.7 against 11.1; of 8000, 2 KV
+  // heads, d = 64, 8 tiles: 12.6 against 9.3).
+  // An SM group whose SMs do not divide by the cluster's leaves some out: 33
+  // clusters of 8 are there at once with two CTAs an SM, 15 with one, 71 and 33 of
+  // 4.  The rooms stay below that, as the last one to wait doubles the time (16
+  // sequences of 1000 tokens, 16 query heads of one KV head: 14.5 us in clusters
+  // of 8, 8.5 of 4).
   const long long heads = static_cast<long long>(num_seqs) * Hkv, head_tiles = (max_tokens + attn::kDecode8Rows - 1) / attn::kDecode8Rows;
-  const long long room = group <= 8 || d == 64 ? 256 : 128;
+  const int per_sm = group <= 8 || d == 64 ? 2 : 1;
+  auto room = [&](int ctas) { return per_sm * (ctas == 8 ? 112 : 128); };
   int most = 8;
-  while (most > 1 && (heads * most > room || most / 2 >= head_tiles)) most /= 2;
-  pl.cluster = heads * most <= room && head_tiles <= 4 * most;
+  while (most > 1 && (heads * most > room(most) || most / 2 >= head_tiles)) most /= 2;
+  const int most_tiles = 2 * heads * most >= room(most) ? 8 : 4;
+  pl.cluster = heads * most <= room(most) && head_tiles <= most_tiles * most;
   pl.hb = pl.cluster ? 1 : decode_heads_per_cta(Hkv);
   const int tokens = attn::kDecode8Rows / pl.hb;
   if (pl.cluster) {
@@ -254,13 +265,21 @@ int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Dec
   e = launch_early(attn::decode8_split_kernel<D, NT, PER_SM, STAGES, false>, static_cast<unsigned>(p.ctas), 1, L::kThreads, L::kAlloc, 1,
                    stream, tk, tv, p);
   if (e != cudaSuccess) return fail_cuda(e);
-  // With few sequences and heads there are many partial rows for each: 16
-  // warps share a head's, else one warp takes them.
-  const bool wide = p.ctas > 16LL * p.S * (p.Hkv / p.hb);
-  const int heads = wide ? 1 : attn::kMerge8Warps;
-  const unsigned gx = static_cast<unsigned>((p.Hq + heads - 1) / heads), gy = static_cast<unsigned>(p.S);
-  e = wide ? launch_early(attn::decode8_merge_kernel<D, 16>, gx, gy, 32 * attn::kMerge8Warps, 0, 1, stream, p)
-           : launch_early(attn::decode8_merge_kernel<D, 1>, gx, gy, 32 * attn::kMerge8Warps, 0, 1, stream, p);
+  // Warps for a head's partial rows, about CTAs / (sequences x groups of heads) of
+  // them: a warp takes 4 or 8 at a time, so one warp makes many trips to memory
+  // where there are many (16 sequences of 1000 tokens, 18 rows: 20.8 us with 1,
+  // 17.1 with 8), and many warps are idle blocks where there are few (the same
+  // with 16: 24.9; 64 of 1000, 5 rows: 42.0 with 8, 34.1 with 2; 4 of 1000, 74
+  // rows: 10.7 with 16, 13.9 with 2).
+  const long long heads = static_cast<long long>(p.S) * (p.Hkv / p.hb);
+  const int per = p.ctas > 48 * heads ? 16 : p.ctas > 12 * heads ? 8 : p.ctas > 2 * heads ? 2 : 1;
+  auto* merge = per == 16  ? attn::decode8_merge_kernel<D, 16>
+                : per == 8 ? attn::decode8_merge_kernel<D, 8>
+                : per == 2 ? attn::decode8_merge_kernel<D, 2>
+                           : attn::decode8_merge_kernel<D, 1>;
+  const int heads_a_block = attn::kMerge8Warps / per;
+  e = launch_early(merge, static_cast<unsigned>((p.Hq + heads_a_block - 1) / heads_a_block), static_cast<unsigned>(p.S),
+                   32 * attn::kMerge8Warps, 0, 1, stream, p);
   if (e != cudaSuccess) return fail_cuda(e);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : fail_cuda(e);

@@ -805,8 +805,9 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
 // Which CTAs of the split pass hold them follows from the lengths, summed up as
 // there; that part needs nothing of the split pass and runs before the wait for
 // it.  Heads that one CTA held alone are written already.  PER warps share a
-// head's partial rows, eight in flight at a time with their LSEs, so that the
-// join costs one trip to memory; the warps are added in their order.
+// head's partial rows, four or eight of each in flight at a time with their LSEs,
+// so that the join costs one or two trips to memory (launch_decode8 chooses PER);
+// the warps are added in their order.
 constexpr int kMerge8Warps = 16;
 
 template <int D, int PER>
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
   if (PER == 1 && pieces <= 1) return;
   // The first piece ends its CTA (slot 1), the others begin theirs (slot 0).
   auto row_of = [&](int i) { return (slot0 + 2 * i + (i == 0 ? 1 : 0)) * per_slot + row0; };
-  constexpr int kFlight = 8;
+  constexpr int kFlight = PER == 16 ? 8 : 4;
   float mx = -INFINITY, sum = 0.f, out[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) out[e] = 0.f;

@@ -387,7 +387,7 @@ DECODES = [
 ]
 
 
-def widen(c, tokens=8192):
+def widen(c, tokens=16384):
     """A table for longer sequences (room for `tokens`): the calls that do not fit a cluster's CTAs, by the sizes alone."""
     S, width = c["table"].shape
     room = -(-tokens // c["ps"])
@@ -402,6 +402,37 @@ def test_decode(Hq, Hkv, d, ps, lens, wide):
     if wide:
         widen(c)
     q = rows(41, len(lens), Hq, d)
+    scale = float(np.float32(d ** -0.5))
+    o, lse = run_decode(c, q, scale)
+    assert api.device_status() == 0
+    assert_decoded(c, q, scale, o, lse)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [
+    (32, 8, 128, [2000]),               # more than 100 partial rows a head
+    (16, 8, 128, [1200, 0, 900, 1, 700]),
+    (32, 8, 128, [300] * 13 + [0, 17, 4000]),  # about 18
+    (8, 2, 64, [1500, 1490, 64, 0, 1, 2000, 777]),
+    (8, 8, 128, [100] * 46 + [1, 2500]),       # about 6
+    (16, 2, 64, [300] * 60),
+    (8, 8, 128, [30] * 199 + [1600]),          # at most a few
+])
+def test_decode_joins_any_number_of_partial_rows(Hq, Hkv, d, lens):
+    """Sequences and heads from 1 to 200, so that each has from over a hundred partial rows down to one."""
+    c = widen(filled_case(44, lens, Hkv, d, 16))
+    q = rows(45, len(lens), Hq, d)
+    scale = float(np.float32(d ** -0.5))
+    o, lse = run_decode(c, q, scale)
+    assert api.device_status() == 0
+    assert_decoded(c, q, scale, o, lse)
+
+
+@pytest.mark.parametrize("S,Hq,Hkv,d", [(13, 16, 1, 128), (14, 16, 1, 128), (16, 16, 1, 128), (32, 8, 1, 128), (33, 2, 1, 64), (64, 4, 1, 64)])
+def test_decode_clusters_more_than_fit_at_once(S, Hq, Hkv, d):
+    """One KV head and up to 64 sequences of up to 1024 tokens: as many clusters as the SMs hold, and more."""
+    lens = [1 + (s * 331) % 1024 for s in range(S)]
+    c = filled_case(46, lens, Hkv, d, 16)
+    q = rows(47, S, Hq, d)
     scale = float(np.float32(d ** -0.5))
     o, lse = run_decode(c, q, scale)
     assert api.device_status() == 0
@@ -496,7 +527,7 @@ def test_decode_empty_batch_and_single_token(wide):
         widen(c)
     o, lse = run_decode(c, rows(77, 3, 4, 64), 0.1)
     assert api.device_status() == 0 and not o.any() and torch.all(lse == -float("inf"))
-    c = widen(filled_case(78, [1], 1, 64, 16), 8192 if wide else 16)  # one token: its value row, and its score
+    c = widen(filled_case(78, [1], 1, 64, 16), 16384 if wide else 16)  # one token: its value row, and its score
     q = rows(79, 1, 1, 64)
     o, lse = run_decode(c, q, 0.1)
     page = int(c["table"][0, 0])
