@@ -294,8 +294,10 @@ constexpr int kGather8Batch = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kGather8Threads) gather8_kernel(const Gather8Params p) {
-  const int row = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-  if (row >= p.total_rows) return;
+  // In warps, unsigned: threads would pass 32 bits at 2^27 rows.
+  const unsigned warp = blockIdx.x * (kGather8Threads / 32) + (threadIdx.x >> 5);
+  if (warp >= static_cast<unsigned>(p.total_rows)) return;
+  const int row = static_cast<int>(warp);
   const int lane = threadIdx.x & 31;
   const int s = warp_find_sequence(p.cu_k, p.num_seqs, row);
   const int r0 = p.cu_k[s], r1 = p.cu_k[s + 1], len = p.seq_lens[s];

@@ -578,6 +578,25 @@ def test_pages_behind_two_gigabytes():
     assert_decoded(small, q, 0.1, o, lse)
 
 
+def test_gather_rows_behind_two_to_the_27():
+    """Outputs of more rows than 2^32 threads of 32 a row: the last sequence's rows lie behind them, the room before is left."""
+    Hkv, d, ps, far = 1, 64, 16, 2 ** 27
+    if torch.cuda.mem_get_info()[0] < 50 * 2 ** 30:
+        pytest.skip("needs 34 GB of outputs")
+    c = filled_case(48, [20, 33], Hkv, d, ps)
+    kp, vp, sc = gpu_cache(c)
+    ko, vo = (torch.empty(far + 64, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for x in (ko, vo):
+        x[:64], x[far - 8:] = MARK, MARK
+    cu = torch.tensor([0, far + 4, far + 40], dtype=torch.int32).cuda()
+    api.paged_kv_gather_fp8(kp, vp, sc, c["table"].cuda(), c["lens"].cuda(), cu, k_out=ko, v_out=vo)
+    assert api.device_status() == 0
+    (k0, v0), (k1, v1) = oracle.paged_gather8(codes(kp), codes(vp), codes(sc), c["table"].numpy(), [20, 33], ps)
+    for x, a, b in ((ko, k0, k1), (vo, v0, v1)):
+        assert np.array_equal(f64(x[:20]), a) and np.array_equal(f64(x[far + 4:far + 37]), b)
+        assert bool((x[20:64] == MARK).all()) and bool((x[far - 8:far + 4] == MARK).all()) and bool((x[far + 37:] == MARK).all())
+
+
 # ------------------------------------------------------- as they are used, together
 
 def test_serving_steps_together():
