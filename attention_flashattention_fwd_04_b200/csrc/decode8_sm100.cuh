@@ -25,7 +25,12 @@
 // byte): S^T = K Q^T and O^T += V^T P^T.
 //   - e4m3 codes become f16 exactly; q, scaled by a power of two of its row to
 //     use f16's range, keeps its 8 bits (values 2^-28 below the row's largest
-//     and less lose some).
+//     and less lose some).  The sum q . kc reaches 2^30 with q so scaled: times 2^ek
+//     it would pass fp32's range long before the score does, so that factor is
+//     2^(ek - b), and 2^b is in the other one, of scale and q's own power.  b is 22, or
+//     what the largest of the KV head's queries leaves of it; so nothing overflows on
+//     the way to a score while scale max|q| max|k|, over a KV head's queries and its
+//     rows, is below 2^127.
 //   - V's scale goes into the weights before they are rounded:
 //     p_t = 2^(s_t + ev_t - m), m a running bound of s_t + ev_t, so that no
 //     weight overflows f16 however far apart the scales are; it is 2^8 off the
@@ -240,8 +245,11 @@ struct Decode8Warp {
   // of the sum, the scores' factor.
   uint64_t nm[NT], l[NT], f[NT];
   uint32_t q[NT][D / 16][2];
+  float kb;  // 2^-b
 
   __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig) {
+    const int scale_exp = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127;
+    int shifts[NT], least = 126;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int h = nt * 8 + grp;
@@ -259,21 +267,33 @@ struct Decode8Warp {
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // Largest magnitude to 2^13 .. 2^14 (as far as 2^shift is a normal float).
+      // Largest magnitude to 2^13 .. 2^14, as far as 2^shift and scale 2^(22 - shift)
+      // are normal floats (what smaller queries lose, 2^-25 of q so scaled, moves a
+      // score by less than 2^-16 scale under the largest keys).
       int shift = 13 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
-      shift = amax == 0.f || amax > 3.4e38f ? 0 : min(shift, 126);
+      shift = amax > 3.4e38f ? 0 : min(amax == 0.f ? 126 : shift, min(126, scale_exp + 148));
+      shifts[nt] = shift;
+      least = min(least, shift);
       const float up = __int_as_float((shift + 127) << 23);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         q[nt][i][0] = pack_f16x2(__uint_as_float(raw[i].x << 16) * up, __uint_as_float(raw[i].x & 0xffff0000u) * up);
         q[nt][i][1] = pack_f16x2(__uint_as_float(raw[i].y << 16) * up, __uint_as_float(raw[i].y & 0xffff0000u) * up);
       }
-      const float factor = scale_log2 * __int_as_float((127 - shift) << 23);  // of head grp; wanted: of heads 2 tig (+ 1)
-      f[nt] = f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4));
       nm[nt] = f2_pack(INFINITY, INFINITY);
       l[nt] = 0;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
+    }
+    // scale 2^(b - shift) < 2^127 for all heads, or at least finite (a row of zeros makes it 0 then).
+    const int b = max(min(22, 126 - scale_exp + __reduce_min_sync(0xffffffffu, least)), 0);
+    kb = __int_as_float((127 - b) << 23);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int e = b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
+      const float factor =  // of head grp; wanted: of heads 2 tig (+ 1)
+          fminf(scale_log2 * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
+      f[nt] = f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4));
     }
   }
 
@@ -309,8 +329,8 @@ struct Decode8Warp {
       __syncwarp();
     }
     const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
-    // K's scales, and V's exponents + 6 as floats (a byte in the last bits of 2^23).
-    const float k0 = cache8_scale(e0 & 255u), k1 = cache8_scale(e1 & 255u);
+    // K's scales times 2^-b, and V's exponents + 6 as floats (a byte in the last bits of 2^23).
+    const float k0 = cache8_scale(e0 & 255u) * kb, k1 = cache8_scale(e1 & 255u) * kb;
     const float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388729.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388729.f;
     const uint64_t k00 = f2_pack(k0, k0), k11 = f2_pack(k1, k1), v00 = f2_pack(v0, v0), v11 = f2_pack(v1, v1);
     uint64_t x[NT][2];  // scores of rows grp and grp + 8 but for f
