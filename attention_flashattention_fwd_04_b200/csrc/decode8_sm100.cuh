@@ -35,7 +35,9 @@
 //     p_t = 2^(s_t + ev_t - m), m a running bound of s_t + ev_t, so that no
 //     weight overflows f16 however far apart the scales are; it is 2^8 off the
 //     largest at most, and the stored weight has 11 bits down to 2^-20 of m.
-//     The softmax's own sum takes 2^(s_t - m) in fp32.
+//     The softmax's own sum takes 2^(s_t - n) in fp32, n a bound of s_t alone: m may
+//     be 119 above the scores or 100 below, where a sum held against it would lose
+//     its smaller terms or overflow.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -75,8 +77,9 @@ struct Decode8Layout {
   static constexpr int kScales = STAGES * kStage;         // 32 bytes a warp and stage
   static constexpr int kBar = kScales + STAGES * 32 * kDecode8Parts;
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
-  static constexpr int kJoin = kWarpSums + 2 * kWarps * 4;    // bounds and sums of the warps, [2][warp][16 heads]
-  static constexpr int kTiles = kJoin + 2 * kWarps * 16 * 4;
+  static constexpr int kHeads = kWarpSums + 2 * kWarps * 4;   // Decode8Heads of the warps, [warp][16 heads / 2]
+  static constexpr int kJoin = kHeads + kWarps * 8 * 32;      // bounds and sums of the warps, [3][warp][16 heads]
+  static constexpr int kTiles = kJoin + 3 * kWarps * 16 * 4;
   // Of a cluster's CTA instead: its share of the values of all CTAs' results (16
   // rows of D floats in all), and their LSEs [8][16].
   static constexpr int kOwn = kTiles, kOwnLse = kOwn + 16 * D * 4;
@@ -237,17 +240,49 @@ __device__ __forceinline__ void cluster_store4(uint32_t addr, const float (&x)[4
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
 }
 
+// Raises a head's bound (kept as its opposite) to the largest `top` of the warp's
+// rows, if that is above it; 2^(old - new).
+__device__ __forceinline__ float decode8_raise(float& minus, float top) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  top = fmaxf(top, -minus);
+  const float factor = ex2_approx(-minus - top);
+  minus = -top;
+  return factor;
+}
+
+// Of two heads, 2 tig (low) and 2 tig + 1 (high): the scores' factor, minus the
+// weights' bound m, minus the sum's bound n.  Of the run: 2^-b (low), and the V
+// exponent (+ 6) below which n has to be looked at (high).
+struct alignas(16) Decode8Heads {
+  uint64_t f, nm, nn, run;
+};
+
 // One tile for one warp.
 template <int D, int NT>
 struct Decode8Warp {
   float acc[NT][D / 16][4];  // O^T: values 16 c + grp (0, 1) and + 8 (2, 3) of heads 2 tig (+ 1)
-  // Of heads 2 tig (low) and 2 tig + 1 (high): minus the bound, this lane's share
-  // of the sum, the scores' factor.
-  uint64_t nm[NT], l[NT], f[NT];
+  uint64_t l[NT];            // this lane's share of the sums of heads 2 tig and 2 tig + 1
   uint32_t q[NT][D / 16][2];
-  float kb;  // 2^-b
+  // Where registers are short the heads' values are in shared memory, a place for
+  // each pair: loads cost less than what is spilled otherwise (64 sequences, d = 128:
+  // 99.3 us against 100.7; 3 x 131072 tokens, two head tiles, d = 64: 29.0 against 33.8).
+  static constexpr bool kShared = NT == 2 || D == 128;
+  Decode8Heads* shared;
+  Decode8Heads own[kShared ? 1 : NT];
 
-  __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig) {
+  __device__ __forceinline__ Decode8Heads heads(int nt) const {
+    if constexpr (kShared) return shared[4 * nt];
+    else return own[nt];
+  }
+  // By the whole warp, all lanes of a pair alike; __syncwarp() before they are read.
+  __device__ __forceinline__ void set_heads(int nt, const Decode8Heads& h, int grp) {
+    if constexpr (!kShared) own[nt] = h;
+    else if (grp == 0) shared[4 * nt] = h;
+  }
+
+  __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig, uint8_t* heads_at) {
+    shared = reinterpret_cast<Decode8Heads*>(heads_at) + tig;
     const int scale_exp = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127;
     int shifts[NT], least = 126;
 #pragma unroll
@@ -280,21 +315,21 @@ struct Decode8Warp {
         q[nt][i][0] = pack_f16x2(__uint_as_float(raw[i].x << 16) * up, __uint_as_float(raw[i].x & 0xffff0000u) * up);
         q[nt][i][1] = pack_f16x2(__uint_as_float(raw[i].y << 16) * up, __uint_as_float(raw[i].y & 0xffff0000u) * up);
       }
-      nm[nt] = f2_pack(INFINITY, INFINITY);
       l[nt] = 0;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
     }
     // scale 2^(b - shift) < 2^127 for all heads, or at least finite (a row of zeros makes it 0 then).
     const int b = max(min(22, 126 - scale_exp + __reduce_min_sync(0xffffffffu, least)), 0);
-    kb = __int_as_float((127 - b) << 23);
+    const uint64_t none = f2_pack(INFINITY, INFINITY), run = f2_pack(__int_as_float((127 - b) << 23), -INFINITY);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int e = b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
       const float factor =  // of head grp; wanted: of heads 2 tig (+ 1)
           fminf(scale_log2 * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
-      f[nt] = f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4));
+      set_heads(nt, {f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4)), none, none, run}, grp);
     }
+    __syncwarp();
   }
 
   // valid: the tokens of the 16 that belong to the sequence (TAIL: fewer than 16).
@@ -330,6 +365,8 @@ struct Decode8Warp {
     }
     const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
     // K's scales times 2^-b, and V's exponents + 6 as floats (a byte in the last bits of 2^23).
+    float kb, v_low;
+    f2_unpack(heads(0).run, kb, v_low);
     const float k0 = cache8_scale(e0 & 255u) * kb, k1 = cache8_scale(e1 & 255u) * kb;
     const float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388729.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388729.f;
     const uint64_t k00 = f2_pack(k0, k0), k11 = f2_pack(k1, k1), v00 = f2_pack(v0, v0), v11 = f2_pack(v1, v1);
@@ -341,52 +378,69 @@ struct Decode8Warp {
     }
     // x f + add for both rows, -inf past the end: a select, since what the slots
     // there hold, their scales too, may be NaN.
-    auto scores = [&](int nt, uint64_t add0, uint64_t add1, float (&out)[4]) {
-      f2_unpack(f2_fma(x[nt][0], f[nt], add0), out[0], out[1]);
-      f2_unpack(f2_fma(x[nt][1], f[nt], add1), out[2], out[3]);
+    auto scores = [&](int nt, uint64_t f, uint64_t add0, uint64_t add1, float (&out)[4]) {
+      f2_unpack(f2_fma(x[nt][0], f, add0), out[0], out[1]);
+      f2_unpack(f2_fma(x[nt][1], f, add1), out[2], out[3]);
       if (TAIL) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[e] = (e < 2 ? t0 : t1) < valid ? out[e] : -INFINITY;
       }
     };
     float w[NT][4];  // log2 of the weights, 2^6 up
+    auto weigh = [&](int nt) {
+      const Decode8Heads h = heads(nt);
+      scores(nt, h.f, f2_add(v00, h.nm), f2_add(v11, h.nm), w[nt]);
+    };
     float top = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      scores(nt, f2_add(v00, nm[nt]), f2_add(v11, nm[nt]), w[nt]);
+      weigh(nt);
       top = max3(top, max3(w[nt][0], w[nt][1], w[nt][2]), w[nt][3]);
     }
-    if (__any_sync(0xffffffffu, top > 14.f)) {  // more than 2^8 off the bound (or none yet): a new one, the largest so far
+    // A weight more than 2^8 off its bound (or none yet), or a value so much smaller
+    // than the largest that set a bound that a score may be far above n although its
+    // weight is not above m: new bounds, the largest so far.  So a score is 105 above
+    // n at most (8 - ev above m, and m that largest exponent above n), and 2^22 terms
+    // of it still add up.
+    if (__any_sync(0xffffffffu, top > 14.f || fminf(v0, v1) < v_low)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float s[4], m[2], a[2];
-        scores(nt, v00, v11, s);
-        f2_unpack(nm[nt], m[0], m[1]);
+        Decode8Heads h = heads(nt);
+        float s[4], m[2], n[2], a[2], b[2];
+        f2_unpack(h.nm, m[0], m[1]);
+        f2_unpack(h.nn, n[0], n[1]);
+        scores(nt, h.f, v00, v11, w[nt]);
+        scores(nt, h.f, 0, 0, s);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float mx = fmaxf(s[u], s[u + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          mx = fmaxf(mx - 6.f, -m[u]);
-          a[u] = ex2_approx(-m[u] - mx);
-          m[u] = -mx;
+          a[u] = decode8_raise(m[u], fmaxf(w[nt][u], w[nt][u + 2]) - 6.f);
+          b[u] = decode8_raise(n[u], fmaxf(s[u], s[u + 2]));
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             acc[nt][c][u] *= a[u];
             acc[nt][c][u + 2] *= a[u];
           }
         }
-        nm[nt] = f2_pack(m[0], m[1]);
-        l[nt] = f2_mul(l[nt], f2_pack(a[0], a[1]));
-        scores(nt, f2_add(v00, nm[nt]), f2_add(v11, nm[nt]), w[nt]);
+        l[nt] = f2_mul(l[nt], f2_pack(b[0], b[1]));
+        h.nm = f2_pack(m[0], m[1]);
+        h.nn = f2_pack(n[0], n[1]);
+        if (nt == 0) {
+          float v = fmaxf(v0, v1);
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+          h.run = f2_pack(kb, fmaxf(v_low, v - 97.f));
+        }
+        set_heads(nt, h, grp);
+        __syncwarp();
+        weigh(nt);
       }
     }
     uint32_t p[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float s[4];
-      scores(nt, nm[nt], nm[nt], s);
+      const Decode8Heads h = heads(nt);
+      scores(nt, h.f, h.nn, h.nn, s);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         w[nt][e] = ex2_approx(w[nt][e]);
@@ -636,7 +690,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   const int hl = warp & (p.hb - 1), chunk = warp >> p.hb_log2, parts = kDecode8Parts >> p.hb_log2;
   const int chunks_per_box = p.box / 16;
   const uint32_t rows_at = ((chunk / chunks_per_box * p.hb + hl) * chunks_per_box + chunk % chunks_per_box) * 16 * D;
-  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [2][warp][16 heads]: bounds, later factors; sums
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [3][warp][16 heads]: m, later factors; sums; n
   int st = 0;          // place in the ring, and phase of its full barriers
   uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
@@ -646,7 +700,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     if (run.from == run.to) continue;
     const int len = p.seq_lens[run.s];
     Decode8Warp<D, NT> w;
-    w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_log2, grp, tig);
+    w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_log2, grp, tig,
+            smem + L::kHeads + warp * 256);
     for (int tile = run.from; tile < run.to; ++tile) {
       if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);
@@ -670,17 +725,17 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     // ring's next NT places), one thread a head works out what each of the
     // head's warps counts, and all threads add up and write O, 8 values at a
     // time.
-    float bound[NT][2], sum[NT][2];
+    float minus_m[NT][2], minus_n[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f2_unpack(w.nm[nt], bound[nt][0], bound[nt][1]);
+      const Decode8Heads h = w.heads(nt);
+      f2_unpack(h.nm, minus_m[nt][0], minus_m[nt][1]);
+      f2_unpack(h.nn, minus_n[nt][0], minus_n[nt][1]);
       f2_unpack(w.l[nt], sum[nt][0], sum[nt][1]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        bound[nt][u] = -bound[nt][u];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) sum[nt][u] += __shfl_xor_sync(0xffffffffu, sum[nt][u], off);
-      }
     }
     uint32_t place[NT];
     decode8_consumers_sync<32 * kDecode8Warps>();  // the last run's factors have been read
@@ -703,8 +758,10 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       if (grp == 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          join[warp * 16 + nt * 8 + 2 * tig + u] = bound[nt][u];
-          join[(kDecode8Warps + warp) * 16 + nt * 8 + 2 * tig + u] = sum[nt][u];
+          const int at = warp * 16 + nt * 8 + 2 * tig + u;
+          join[at] = -minus_m[nt][u];
+          join[kDecode8Warps * 16 + at] = sum[nt][u];
+          join[2 * kDecode8Warps * 16 + at] = -minus_n[nt][u];
         }
       }
     }
@@ -720,12 +777,12 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       const int index = min(static_cast<int>(threadIdx.x), 8 * p.group - 1);
       const int part = index & (parts - 1), row = index >> (3 - p.hb_log2);
       const int g = row / p.group, mine_at = (part * p.hb + g) * 16 + row - g * p.group;
-      const float m = join[mine_at];
-      float mx = m;
+      const float m = join[mine_at], n = join[2 * kDecode8Warps * 16 + mine_at];
+      float mx = n;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1)
         if (off < parts) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      float sum = join[kDecode8Warps * 16 + mine_at] * ex2_approx(m - mx);
+      float sum = join[kDecode8Warps * 16 + mine_at] * ex2_approx(n - mx);
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1)
         if (off < parts) sum += __shfl_xor_sync(0xffffffffu, sum, off);

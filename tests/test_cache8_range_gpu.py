@@ -9,7 +9,7 @@ import torch
 
 from attention_flashattention_fwd_04_b200 import api
 
-from .test_cache8_gpu import assert_decoded, cache_case, oracle_append, rows, run_decode, widen
+from .test_cache8_gpu import assert_decoded, cache_case, f64, oracle_append, rows, run_decode, widen
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,49 @@ def test_saturated_keys(wide):
     o, lse = run_decode(widen(c) if wide else c, q, scale)
     assert api.device_status() == 0 and torch.isfinite(o).all() and torch.isfinite(lse).all()
     assert_decoded(c, q, scale, o, lse)
+
+
+def one_hot(c, L, d, Hkv, scores, v):
+    """Scores of the caller's choice: q is the first unit vector, the scale 1, and k's first value the score."""
+    k = torch.zeros(L, Hkv, d)
+    k[:, :, 0] = scores[:, None]
+    assert torch.equal(k.to(torch.bfloat16).float(), k)
+    c = stored(c, k, v)
+    q = torch.zeros(1, 4 * Hkv, d)
+    q[..., 0] = 1.0
+    return c, q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("exponent", [-120, -95, 0, 90, 119, 126])
+def test_many_small_weights_under_any_value_scale(exponent, d, ps, wide):
+    """One token 9 above thousands: together they weigh as much as a third of it, however large or small the values are."""
+    L = 3000
+    c = cache_case(220, [0], [L], 2, d, ps)
+    g = torch.Generator().manual_seed(221)
+    v = torch.ldexp(torch.randn(L, 2, d, generator=g).clamp(-1.9, 1.9), torch.tensor(exponent))
+    scores = torch.zeros(L)
+    scores[1234] = 9.0
+    c, q = one_hot(c, L, d, 2, scores, v)
+    o, lse = run_decode(widen(c) if wide else c, q, 1.0)
+    assert_decoded(c, q, 1.0, o, lse)
+    assert np.allclose(f64(lse), np.log(np.exp(9.0) + L - 1), atol=2.0 ** -17)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("first,last", [(119, -100), (-100, 119), (119, 0), (0, -100), (-100, 0)])
+@pytest.mark.parametrize("rise", [0.0, 60.0, -60.0, 240.0])
+def test_value_scales_and_scores_that_change_along_the_sequence(first, last, rise, wide):
+    """Values of one scale under scores of one height, then of another under another."""
+    L, half, d = 1500, 700, 64
+    c = cache_case(230, [0], [L], 2, d, 16)
+    g = torch.Generator().manual_seed(231)
+    v = torch.randn(L, 2, d, generator=g).clamp(-1.9, 1.9)
+    v = torch.cat([torch.ldexp(v[:half], torch.tensor(first)), torch.ldexp(v[half:], torch.tensor(last))])
+    scores = torch.randint(-2, 3, (L,), generator=g).float()
+    scores[half:] += rise
+    scores = scores.to(torch.bfloat16).float()
+    c, q = one_hot(c, L, d, 2, scores, v)
+    o, lse = run_decode(widen(c) if wide else c, q, 1.0)
+    assert_decoded(c, q, 1.0, o, lse)
