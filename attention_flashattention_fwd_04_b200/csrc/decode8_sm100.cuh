@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float w = ex2_approx(l[c] - top);
+        const float w = ex2_approx(l[c] - top) * 0x1p-4f;  // 8 results of the largest values still add up
         sum += w;
         x[0] = fmaf(w, a[c].x, x[0]);
         x[1] = fmaf(w, a[c].y, x[1]);
@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       const float inv = 1.f / sum;
       *reinterpret_cast<uint2*>(p.o + (head + row) * D + 4 * (slot * p.ctas + rank)) =
           make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-      if (slot == 0 && rank == 0) p.lse[head + row] = (top + log2f(sum)) * 0.69314718055994530942f;
+      if (slot == 0 && rank == 0) p.lse[head + row] = (top + log2f(sum * 0x1p4f)) * 0.69314718055994530942f;
     }
   }
 }
@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
       for (int e = 0; e < kPer; ++e) out[e] *= a;
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
-        const float w = ex2_approx(l[u] - mx);
+        const float w = ex2_approx(l[u] - mx - 12.f);  // 2^-12: hundreds of rows of the largest values still add up
         sum += w;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) out[e] = fmaf(w, x[u][e], out[e]);
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
 #pragma unroll
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(p.o + head * D + lane * kPer + e) = pack_bf16x2(out[e] * inv, out[e + 1] * inv);
-  if (lane == 0) p.lse[head] = (mx + log2f(sum)) * 0.69314718055994530942f;
+  if (lane == 0) p.lse[head] = (mx + log2f(sum * 0x1p12f)) * 0.69314718055994530942f;
 }
 
 }  // namespace attn

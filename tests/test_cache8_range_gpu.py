@@ -13,6 +13,8 @@ from .test_cache8_gpu import assert_decoded, cache_case, f64, oracle_append, row
 
 pytestmark = pytest.mark.gpu
 
+TOP = 448.0 * 2.0 ** 119  # the cache's largest value
+
 
 def stored(c, k, v):
     """The case with the rows k and v [T, Hkv, d] quantised in its cache, every other slot NaN codes under the scale 255."""
@@ -100,3 +102,22 @@ def test_value_scales_and_scores_that_change_along_the_sequence(first, last, ris
     c, q = one_hot(c, L, d, 2, scores, v)
     o, lse = run_decode(widen(c) if wide else c, q, 1.0)
     assert_decoded(c, q, 1.0, o, lse)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("d,L", [(64, 1000), (128, 2000), (128, 30)])
+def test_the_largest_values_and_none(d, L, wide):
+    """Every value the largest there is: so is O, not an infinity on the way.  Values of zero: O is zero, LSE that of the scores."""
+    c = cache_case(240, [0], [L], 2, d, 16)
+    g = torch.Generator().manual_seed(241)
+    scores = torch.randint(-8, 9, (L,), generator=g).float()
+    v = torch.full((L, 2, d), float("inf"))
+    v[:, :, 1::2] = -float("inf")
+    v[:, 1] = 0.0
+    c, q = one_hot(c, L, d, 2, scores, v)
+    o, lse = run_decode(widen(c) if wide else c, q, 1.0)
+    o, lse = f64(o), f64(lse)
+    want = np.log(np.exp(scores.double().numpy()).sum())
+    assert np.allclose(lse, want, atol=2.0 ** -17)
+    assert np.all(np.abs(o[0, :4, ::2] / TOP - 1) <= 2.0 ** -8) and np.all(np.abs(o[0, :4, 1::2] / -TOP - 1) <= 2.0 ** -8)
+    assert not o[0, 4:].any()
