@@ -638,7 +638,8 @@ def rope_spec(d: int, sections=None, theta: float = 10000.0, rot_dim: int | None
     order of the positions' axes (default: one axis).  They follow one another,
     or, with ``interleaved_sections``, take turns while they last (t h w t h w
     ...).  ``inv_freq``: the rot_dim / 2 frequencies in radians a position
-    (default theta ** (-2 j / rot_dim)), e.g. rescaled ones for long contexts.
+    (default theta ** (-2 j / rot_dim)), e.g. rescaled ones for long contexts;
+    magnitudes below 2^62.
     ``adjacent_pairs``: pairs (2j, 2j + 1) instead of (j, j + rot_dim / 2).
     """
     rot = d if rot_dim is None else int(rot_dim)

@@ -15,8 +15,28 @@ namespace {
 // Rotary positions
 // ----------------------------------------------------------------------------
 
-// Checks a rotation and lays its table out for the kernels: frequencies in
-// turns, as fractions of 2^64 (long double holds all 64 bits).
+// inv_freq / 2 pi modulo 1, in units of 2^-64, to the nearest, for |inv_freq| <
+// 2^62: the product of the frequency's 53 bits and the first 128 of 1 / 2 pi, shifted.
+// (A quotient in 64 bits would lose one of the fraction's for each bit of whole turns.)
+uint64_t rope_turn(double inv_freq) {
+  constexpr uint64_t kInverse[2] = {0x28be60db9391054aull, 0x7f09d5f47d4d3770ull};  // 1 / 2 pi
+  int e;
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(std::frexp(std::fabs(inv_freq), &e), 53));
+  const int shift = 53 - e + 64;  // inv_freq / 2 pi * 2^64 = m * kInverse / 2^shift, shift >= 55
+  if (shift > 190) return 0;      // below half a unit
+  const unsigned __int128 low = static_cast<unsigned __int128>(m) * kInverse[1];
+  const unsigned __int128 high = static_cast<unsigned __int128>(m) * kInverse[0] + static_cast<uint64_t>(low >> 64);
+  const uint64_t words[4] = {static_cast<uint64_t>(low), static_cast<uint64_t>(high), static_cast<uint64_t>(high >> 64), 0};
+  auto from = [&](int bit) {  // 64 bits of the product
+    const int w = bit / 64, b = bit % 64;
+    if (w > 2) return uint64_t{0};
+    return b == 0 ? words[w] : words[w] >> b | words[w + 1] << (64 - b);
+  };
+  const uint64_t turn = from(shift) + (from(shift - 1) & 1u);
+  return inv_freq < 0 ? 0 - turn : turn;
+}
+
+// Checks a rotation and lays its table out for the kernels.
 int rope_table(const attn_rope_spec* spec, int d, attn::RopeTable* out) {
   if (!spec) return ATTN_ERR_NULL;
   if (spec->rot_dim < 16 || spec->rot_dim > d || spec->rot_dim % 16 != 0) return ATTN_ERR_SHAPE;
@@ -26,10 +46,8 @@ int rope_table(const attn_rope_spec* spec, int d, attn::RopeTable* out) {
   out->half = spec->rot_dim / 2;
   out->adjacent = spec->adjacent_pairs;
   for (int j = 0; j < out->half; ++j) {
-    if (!std::isfinite(spec->inv_freq[j]) || spec->axis[j] >= spec->num_axes) return ATTN_ERR_SHAPE;
-    long double turns = static_cast<long double>(spec->inv_freq[j]) / 6.283185307179586476925286766559L;
-    turns = ldexpl(turns - floorl(turns), 64);
-    out->turn[j] = turns >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(turns + 0.5L);
+    if (!(std::fabs(spec->inv_freq[j]) < 0x1p62) || spec->axis[j] >= spec->num_axes) return ATTN_ERR_SHAPE;
+    out->turn[j] = rope_turn(spec->inv_freq[j]);
     out->axis[j] = spec->axis[j];
   }
   return ATTN_OK;

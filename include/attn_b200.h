@@ -359,7 +359,7 @@ int paged_prefill_append(const attn_bf16* q, const attn_bf16* k_new, const attn_
  * frequencies in any order.
  *   rot_dim   a multiple of 16, 16 .. d
  *   num_axes  1 .. 255
- *   inv_freq, axis: rot_dim / 2 entries used; finite; axis[j] < num_axes
+ *   inv_freq, axis: rot_dim / 2 entries used; |inv_freq| < 2^62; axis[j] < num_axes
  */
 typedef struct attn_rope_spec {
   int rot_dim;
