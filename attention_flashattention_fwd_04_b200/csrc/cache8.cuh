@@ -296,6 +296,13 @@ template <int D>
 __global__ void __launch_bounds__(kGather8Threads) gather8_kernel(const Gather8Params p) {
   // In warps, unsigned: threads would pass 32 bits at 2^27 rows.
   const unsigned warp = blockIdx.x * (kGather8Threads / 32) + (threadIdx.x >> 5);
+  // Tokens that have no row have no warp that looks at them: the last block does.
+  if (blockIdx.x == gridDim.x - 1) {
+    for (int i = threadIdx.x; i < p.num_seqs; i += kGather8Threads) {
+      const int n = p.seq_lens[i], first = p.cu_k[i];
+      if ((n != 0 && p.cu_k[i + 1] <= first) || (n > 0 && first > p.total_rows - n)) atomicOr(&g_attn_device_error, kErrCache8Table);
+    }
+  }
   if (warp >= static_cast<unsigned>(p.total_rows)) return;
   const int row = static_cast<int>(warp);
   const int lane = threadIdx.x & 31;

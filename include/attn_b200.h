@@ -443,10 +443,12 @@ int paged_rope_append_fp8(const attn_bf16* q, const attn_bf16* k_new, const attn
  *   cu_seqlens_k  [num_seqs + 1] int32, non-decreasing from 0, at most
  *                 total_rows; a sequence may have more room than tokens (rows
  *                 behind its tokens, and behind the last sequence, stay as they
- *                 were), less is reported and skipped.  With starts rounded up to
+ *                 were), less (none at all, too) is reported and skipped, and so
+ *                 are tokens that total_rows cuts off.  With starts rounded up to
  *                 a page size the output is itself a bf16 pool, which
  *                 paged_prefill and paged_attn_decode read.
- * seq_len = 0 is a sequence without tokens.  Errors as above.
+ * seq_len = 0 is a sequence without tokens; total_rows = 0 does nothing.  Errors
+ * as above.
  */
 int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint8_t* kv_scales, const int32_t* block_table,
                         const int32_t* seq_lens, const int32_t* cu_seqlens_k, attn_bf16* k_out, attn_bf16* v_out,
