@@ -697,7 +697,7 @@ def _on_stream(fn):
     def wrapped(*args, stream=None, **kwargs):
         if stream is None:
             return fn(*args, **kwargs)
-        for a in args:
+        for a in (*args, *kwargs.values()):
             if isinstance(a, torch.Tensor) and a.is_cuda and a.device != stream.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {a.device}")
         with torch.cuda.stream(stream):
