@@ -64,6 +64,8 @@ LONG = [
     (7, 1, 64, 256, 6, 1, [131072, 131071, 5, 0, 100000, 77777, 128]),
     (32, 2, 64, 64, 6, 2, [65537, 1, 64, 0, 90001, 80000, 63]),
     (64, 4, 64, 32, 6, 4, [60000, 70011, 0, 31, 55555]),
+    (16, 16, 128, 32, 3, 8, [20000 + 777 * i % 9000 for i in range(5)] + [1, 0]),
+    (36, 12, 64, 48, 6, 4, [23000, 30011, 47, 0, 25555, 1]),
 ]
 
 
