@@ -713,8 +713,11 @@ def attn_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, 
     q [B,Hq,N,d] and k [B,Hkv,N,d] bf16 with positions [axes,B,N] int32, or
     packed q [T,Hq,d], k [T,Hkv,d] with positions [axes,T]; ``k`` may be None.
     Rows must be contiguous, the other strides are free (multiples of 8).
-    ``inverse`` turns back, which is the gradient.  ``q_out`` / ``k_out`` may be
-    q / k.  ``stream``: a torch.cuda.Stream (default: the current one).
+    ``inverse`` turns back, which is the gradient: like every call here this one
+    leaves nothing for autograd, also where q or k ask for a gradient, and dL/dq and
+    dL/dk are ``attn_rope(dL/dq_out, dL/dk_out, positions, spec, inverse=True)``.
+    ``q_out`` / ``k_out`` may be q / k.  ``stream``: a torch.cuda.Stream (default:
+    the current one).
     Returns (q_out, k_out), bf16."""
     rc, q_out, k_out = (_marshal or _marshaller()).rope(q, k, positions, _spec_address(spec), inverse, q_out, k_out)
     if rc != ATTN_OK:
@@ -743,8 +746,8 @@ def kv_cache_fp8(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda"
 def paged_kv_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                         kv_scales: torch.Tensor, block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
                         seq_lens: torch.Tensor):
-    """paged_kv_append into an 8-bit cache: quantises the new rows (packed
-    [total_q,Hkv,d] bf16) as they are written.  k_pool / v_pool
+    """paged_kv_append into an 8-bit cache: quantises the new rows (packed and
+    contiguous, [total_q,Hkv,d] bf16) as they are written.  k_pool / v_pool
     [num_pages,page_size,Hkv,d] float8_e4m3fn and kv_scales
     [num_pages,Hkv,page_size,2] float8_e8m0fnu (uint8 views of them are taken
     too), see kv_cache_fp8.  In place.  ``stream`` as in attn_rope."""
@@ -759,7 +762,8 @@ def paged_rope_append_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Ten
                           block_table: torch.Tensor, cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor,
                           q_out: torch.Tensor | None = None):
     """attn_rope on a step's q [total_q,Hq,d] and k_new and
-    paged_kv_append_fp8, in one kernel (positions [axes,total_q] int32).  The
+    paged_kv_append_fp8, in one kernel (positions [axes,total_q] int32; q, k_new and
+    v_new contiguous: slices of a fused projection are copied first).  The
     cache is updated in place; ``q_out`` may be q.  ``stream`` as in attn_rope.
     Returns q_out; its rows behind cu_seqlens_q[-1] are not written."""
     rc, q_out = (_marshal or _marshaller()).rope_append(q, k_new, v_new, positions, _spec_address(spec), k_pool, v_pool, kv_scales,

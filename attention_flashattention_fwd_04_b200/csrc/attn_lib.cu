@@ -119,13 +119,17 @@ cudaError_t launch_early(void (*kernel)(Params...), unsigned grid_x, unsigned gr
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// SMs of a B200.  Plans, and with them workspaces, follow from the sizes alone and
+// ask no device; on a part of one (fewer SMs) the same grids take more rounds.
+constexpr int kPlanSms = 148;
+
 // Tokens of a block of the kernels on rows: 16, so that their angles are shared
 // by many rows and a head's tokens make long runs (4 x 16 + 16 heads x 2048
-// tokens of d = 128: 24.1 us, with 8 tokens 26.4), but few enough that small
-// calls have two blocks an SM.
+// tokens of d = 128: 24.1 us, with 8 tokens 26.4), but no more than leave two
+// blocks for each SM; below 16 tokens that gives two to four.
 int row_tokens_log2(long long tokens) {
   int n = 4;
-  while (n > 0 && tokens >> n < 2 * 148) --n;
+  while (n > 0 && tokens >> n < 2 * kPlanSms) --n;
   return n;
 }
 
@@ -214,14 +218,14 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   // Clusters, where one a sequence and KV head fills no more than the SMs hold
   // and a CTA has few tiles: no partial results and no second launch, but no even
   // shares either.  Up to 8 tiles where they fill half the SMs or more (16
-  // sequences of 2000 tokens, 8 KV heads: 17.5 us against 22.3; one of 2000 among
-  // 15 of 100: 12.8 against 12.5; with up to 16, one of 4000 among 15: 20.2 against
-  // 13.4), else 4 (one of 4000 tokens, 8 KV heads: 8.7 against 11.1; of 8000, 2 KV
-  // heads, d = 64, 8 tiles: 12.6 against 9.3).
+  // sequences of 2000 tokens, 8 KV heads: 17.6 us against 21.9; one of 2000 among
+  // 15 of 100: 12.7 against 12.8; with up to 16, one of 4000 among 15: 20.1 against
+  // 13.3), else 4 (one of 4000 tokens, 8 KV heads: 8.6 against 10.9; of 8000, 2 KV
+  // heads, d = 64, 8 tiles: 12.4 against 9.4).
   // An SM group whose SMs do not divide by the cluster's leaves some out: 33
   // clusters of 8 are there at once with two CTAs an SM, 15 with one, 71 and 33 of
   // 4.  The rooms stay below that, as the last one to wait doubles the time (16
-  // sequences of 1000 tokens, 16 query heads of one KV head: 14.5 us in clusters
+  // sequences of 1000 tokens, 16 query heads of one KV head: 14.9 us in clusters
   // of 8, 8.5 of 4).
   const long long heads = static_cast<long long>(num_seqs) * Hkv, head_tiles = (max_tokens + attn::kDecode8Rows - 1) / attn::kDecode8Rows;
   const int per_sm = group <= 8 || d == 64 ? 2 : 1;
@@ -243,7 +247,7 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   const long long tiles = std::min(num_seqs, attn::kDecode8MaxSeqs) * ((max_tokens + tokens - 1) / tokens) * (Hkv / pl.hb);
   if (tiles + 3LL * attn::kDecode8MaxSeqs * (Hkv / pl.hb) > INT_MAX) return false;  // units of work, in 32 bits
   // Every CTA that the SMs hold at once (see paged_attn_decode_fp8), or one a tile.
-  pl.ctas = static_cast<int>(std::min<long long>(tiles, d == 64 || group <= 8 ? 2 * 148 : 148));
+  pl.ctas = static_cast<int>(std::min<long long>(tiles, d == 64 || group <= 8 ? 2 * kPlanSms : kPlanSms));
   const size_t rows = 2 * static_cast<size_t>(pl.ctas) * pl.hb * group;
   pl.lse_offset = rows * d * sizeof(float);
   pl.total = (pl.lse_offset + rows * sizeof(float) + 15) & ~static_cast<size_t>(15);
@@ -285,10 +289,10 @@ int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Dec
   if (e != cudaSuccess) return fail_cuda(e);
   // Warps for a head's partial rows, about CTAs / (sequences x groups of heads) of
   // them: a warp takes 4 or 8 at a time, so one warp makes many trips to memory
-  // where there are many (16 sequences of 1000 tokens, 18 rows: 20.8 us with 1,
-  // 17.1 with 8), and many warps are idle blocks where there are few (the same
-  // with 16: 24.9; 64 of 1000, 5 rows: 42.0 with 8, 34.1 with 2; 4 of 1000, 74
-  // rows: 10.7 with 16, 13.9 with 2).
+  // where there are many (16 sequences of 1000 tokens, 18 rows: 20.1 us with 1,
+  // 16.9 with 8), and many warps are idle blocks where there are few (the same
+  // with 16: 24.7; 64 of 1000, 5 rows: 40.9 with 8, 33.0 with 2; 4 of 1000, 74
+  // rows: 10.2 with 16, 15.7 with 2).
   const long long heads = static_cast<long long>(p.S) * (p.Hkv / p.hb);
   const int per = p.ctas > 48 * heads ? 16 : p.ctas > 12 * heads ? 8 : p.ctas > 2 * heads ? 2 : 1;
   auto* merge = per == 16  ? attn::decode8_merge_kernel<D, 16>

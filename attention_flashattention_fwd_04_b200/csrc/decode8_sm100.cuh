@@ -8,21 +8,23 @@
 // whatever the sequences' lengths (they are read and summed up on the device),
 // so that all SMs finish together.  Where a share is many tiles, the begin of a
 // sequence counts as up to 3 more: that is what it costs to write one result and
-// set up the next (3 sequences of 70001 to 131072 tokens, 16 query heads a KV
-// head: 28.8 us without, 27.6 with it).  A run that covers the whole of a sequence's
+// set up the next (16 sequences of 4000 to 8200 tokens, 16 query heads a KV head of
+// d = 128: 34.4 us without, 31.8 with it).  A run that covers the whole of a sequence's
 // tiles writes its output; others write partial results, at most two a CTA,
 // which decode8_merge_kernel joins.
 //
 // Few and short sequences go without the merge: a cluster of up to 8 CTAs has one
 // sequence and KV head, and joins its results through its CTAs' shared memory
-// (one sequence of 1000 tokens: 6.3 us against 8.1, and one launch less).
+// (one sequence of 1000 tokens: 6.3 us against 7.9, and one launch less).
 //
 // A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
 // each of the 8 consumer warps works on 16 of the tile's rows, 16 tokens of one
 // KV head, for 8 NT of its query heads.  Both products run on mma.sync m16n8k16
-// with the cache as the 16-row operand and the query heads as columns (tcgen05's
-// tiles are far larger than a group of query heads, and there are a few FLOP per
-// byte): S^T = K Q^T and O^T += V^T P^T.
+// with the cache as the 16-row operand and the query heads as columns: S^T = K Q^T
+// and O^T += V^T P^T.  There are a few FLOP per byte of cache, and a warp's operands
+// go from its ring place to its registers and are converted there; a tcgen05 form
+// would take 8-bit codes only against queries and weights of 8 bits, or as f16 that
+// threads write back to shared or tensor memory first.  It has not been built.
 //   - e4m3 codes become f16 exactly; q, scaled by a power of two of its row to
 //     use f16's range, keeps its 8 bits (values 2^-28 below the row's largest
 //     and less lose some).  The sum q . kc reaches 2^30 with q so scaled: times 2^ek
@@ -708,8 +710,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       if (!ok) continue;
       const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + warp) * 32;
       const int valid = len - tile * tokens - chunk * 16;
-      // Two head tiles gain by a path without the selects; one loses more by the
-      // code's size and its registers (64 sequences, NT = 1: 104 against 101 us).
+      // Two head tiles have a path without the selects; one loses by the code's size
+      // (one sequence of 1000 tokens: 6.5 against 6.3 us; 64 sequences: 99.8 against 99.3).
       if (NT == 2 && valid >= 16)
         w.template tile<false>(k, k + L::kPool, sc, 16, lane);
       else if (valid > 0)
