@@ -40,6 +40,10 @@
 //     The softmax's own sum takes 2^(s_t - n) in fp32, n a bound of s_t alone: m may
 //     be 119 above the scores or 100 below, where a sum held against it would lose
 //     its smaller terms or overflow.
+//   - Both exponents come from one fma each.  Where n is far from 0 its rounding, and
+//     that of m, would weigh more than the bf16 result's, and beyond 2^27 the fma's
+//     unrounded product be far from n: there (above 2^9) scores are rounded first,
+//     and m is taken as n + (m - n).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -79,8 +83,8 @@ struct Decode8Layout {
   static constexpr int kScales = STAGES * kStage;         // 32 bytes a warp and stage
   static constexpr int kBar = kScales + STAGES * 32 * kDecode8Parts;
   static constexpr int kWarpSums = kBar + 2 * STAGES * 8;
-  static constexpr int kHeads = kWarpSums + 2 * kWarps * 4;   // Decode8Heads of the warps, [warp][16 heads / 2]
-  static constexpr int kJoin = kHeads + kWarps * 8 * 32;      // bounds and sums of the warps, [3][warp][16 heads]
+  static constexpr int kHeads = kWarpSums + 2 * kWarps * 4;   // of the warps: Decode8Heads [16 heads / 2], and Decode8Factors
+  static constexpr int kJoin = kHeads + kWarps * (8 * 32 + 16);  // bounds and sums of the warps, [3][warp][16 heads]
   static constexpr int kTiles = kJoin + 3 * kWarps * 16 * 4;
   // Of a cluster's CTA instead: its share of the values of all CTAs' results (16
   // rows of D floats in all), and their LSEs [8][16].
@@ -242,22 +246,21 @@ __device__ __forceinline__ void cluster_store4(uint32_t addr, const float (&x)[4
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
 }
 
-// Raises a head's bound (kept as its opposite) to the largest `top` of the warp's
-// rows, if that is above it; 2^(old - new).
-__device__ __forceinline__ float decode8_raise(float& minus, float top) {
+// The largest x of the warp's rows.
+__device__ __forceinline__ float decode8_top(float x) {
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  top = fmaxf(top, -minus);
-  const float factor = ex2_approx(-minus - top);
-  minus = -top;
-  return factor;
+  for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
 }
 
 // Of two heads, 2 tig (low) and 2 tig + 1 (high): the scores' factor, minus the
-// weights' bound m, minus the sum's bound n.  Of the run: 2^-b (low), and the V
-// exponent (+ 6) below which n has to be looked at (high).
+// weights' bound m, minus the sum's bound n, and m - n.
 struct alignas(16) Decode8Heads {
-  uint64_t f, nm, nn, run;
+  uint64_t f, nm, nn, d;
+};
+// Of the run: 2^-b, and the V exponent (+ 6) below which the bounds have to be looked at.
+struct alignas(8) Decode8Factors {
+  float kb, v_low;
 };
 
 // One tile for one warp.
@@ -272,6 +275,8 @@ struct Decode8Warp {
   static constexpr bool kShared = NT == 2 || D == 128;
   Decode8Heads* shared;
   Decode8Heads own[kShared ? 1 : NT];
+  Decode8Factors* shared_factors;
+  Decode8Factors own_factors;
 
   __device__ __forceinline__ Decode8Heads heads(int nt) const {
     if constexpr (kShared) return shared[4 * nt];
@@ -282,9 +287,15 @@ struct Decode8Warp {
     if constexpr (!kShared) own[nt] = h;
     else if (grp == 0) shared[4 * nt] = h;
   }
+  __device__ __forceinline__ Decode8Factors factors() const { return kShared ? *shared_factors : own_factors; }
+  __device__ __forceinline__ void set_factors(const Decode8Factors& f, int lane) {
+    if constexpr (!kShared) own_factors = f;
+    else if (lane == 0) *shared_factors = f;
+  }
 
   __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig, uint8_t* heads_at) {
     shared = reinterpret_cast<Decode8Heads*>(heads_at) + tig;
+    shared_factors = reinterpret_cast<Decode8Factors*>(heads_at + 8 * 32);
     const int scale_exp = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127;
     int shifts[NT], least = 126;
 #pragma unroll
@@ -323,13 +334,14 @@ struct Decode8Warp {
     }
     // scale 2^(b - shift) < 2^127 for all heads, or at least finite (a row of zeros makes it 0 then).
     const int b = max(min(22, 126 - scale_exp + __reduce_min_sync(0xffffffffu, least)), 0);
-    const uint64_t none = f2_pack(INFINITY, INFINITY), run = f2_pack(__int_as_float((127 - b) << 23), -INFINITY);
+    const uint64_t none = f2_pack(INFINITY, INFINITY);
+    set_factors({__int_as_float((127 - b) << 23), -INFINITY}, 4 * grp + tig);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int e = b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
       const float factor =  // of head grp; wanted: of heads 2 tig (+ 1)
           fminf(scale_log2 * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
-      set_heads(nt, {f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4)), none, none, run}, grp);
+      set_heads(nt, {f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4)), none, none, 0}, grp);
     }
     __syncwarp();
   }
@@ -367,9 +379,8 @@ struct Decode8Warp {
     }
     const uint32_t e0 = lds_u16(scales + 2 * t0), e1 = lds_u16(scales + 2 * t1);
     // K's scales times 2^-b, and V's exponents + 6 as floats (a byte in the last bits of 2^23).
-    float kb, v_low;
-    f2_unpack(heads(0).run, kb, v_low);
-    const float k0 = cache8_scale(e0 & 255u) * kb, k1 = cache8_scale(e1 & 255u) * kb;
+    const Decode8Factors of_run = factors();
+    const float k0 = cache8_scale(e0 & 255u) * of_run.kb, k1 = cache8_scale(e1 & 255u) * of_run.kb;
     const float v0 = __uint_as_float(0x4b000000u | e0 >> 8) - 8388729.f, v1 = __uint_as_float(0x4b000000u | e1 >> 8) - 8388729.f;
     const uint64_t k00 = f2_pack(k0, k0), k11 = f2_pack(k1, k1), v00 = f2_pack(v0, v0), v11 = f2_pack(v1, v1);
     uint64_t x[NT][2];  // scores of rows grp and grp + 8 but for f
@@ -378,79 +389,92 @@ struct Decode8Warp {
       x[nt][0] = f2_mul(f2_pack(sc[nt][0], sc[nt][1]), k00);
       x[nt][1] = f2_mul(f2_pack(sc[nt][2], sc[nt][3]), k11);
     }
-    // x f + add for both rows, -inf past the end: a select, since what the slots
-    // there hold, their scales too, may be NaN.
-    auto scores = [&](int nt, uint64_t f, uint64_t add0, uint64_t add1, float (&out)[4]) {
-      f2_unpack(f2_fma(x[nt][0], f, add0), out[0], out[1]);
-      f2_unpack(f2_fma(x[nt][1], f, add1), out[2], out[3]);
+    // Past the end -inf: a select, since what the slots there hold, their scales too,
+    // may be NaN.
+    auto within = [&](float (&out)[4]) {
       if (TAIL) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[e] = (e < 2 ? t0 : t1) < valid ? out[e] : -INFINITY;
       }
     };
-    float w[NT][4];  // log2 of the weights, 2^6 up
-    auto weigh = [&](int nt) {
-      const Decode8Heads h = heads(nt);
-      scores(nt, h.f, f2_add(v00, h.nm), f2_add(v11, h.nm), w[nt]);
+    auto scores = [&](int nt, uint64_t f, uint64_t add0, uint64_t add1, float (&out)[4]) {
+      f2_unpack(f2_fma(x[nt][0], f, add0), out[0], out[1]);
+      f2_unpack(f2_fma(x[nt][1], f, add1), out[2], out[3]);
+      within(out);
     };
-    float top = -INFINITY;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      weigh(nt);
-      top = max3(top, max3(w[nt][0], w[nt][1], w[nt][2]), w[nt][3]);
-    }
-    // A weight more than 2^8 off its bound (or none yet), or a value so much smaller
-    // than the largest that set a bound that a score may be far above n although its
-    // weight is not above m: new bounds, the largest so far.  So a score is 105 above
-    // n at most (8 - ev above m, and m that largest exponent above n), and 2^22 terms
-    // of it still add up.
-    if (__any_sync(0xffffffffu, top > 14.f || fminf(v0, v1) < v_low)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        Decode8Heads h = heads(nt);
-        float s[4], m[2], n[2], a[2], b[2];
-        f2_unpack(h.nm, m[0], m[1]);
-        f2_unpack(h.nn, n[0], n[1]);
-        scores(nt, h.f, v00, v11, w[nt]);
-        scores(nt, h.f, 0, 0, s);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          a[u] = decode8_raise(m[u], fmaxf(w[nt][u], w[nt][u + 2]) - 6.f);
-          b[u] = decode8_raise(n[u], fmaxf(s[u], s[u + 2]));
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            acc[nt][c][u] *= a[u];
-            acc[nt][c][u + 2] *= a[u];
-          }
-        }
-        l[nt] = f2_mul(l[nt], f2_pack(b[0], b[1]));
-        h.nm = f2_pack(m[0], m[1]);
-        h.nn = f2_pack(n[0], n[1]);
-        if (nt == 0) {
-          float v = fmaxf(v0, v1);
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-          h.run = f2_pack(kb, fmaxf(v_low, v - 97.f));
-        }
-        set_heads(nt, h, grp);
-        __syncwarp();
-        weigh(nt);
-      }
-    }
     uint32_t p[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float s[4];
-      const Decode8Heads h = heads(nt);
-      scores(nt, h.f, h.nn, h.nn, s);
+    // From the log2 of the weights, 2^6 up, and of the sum's terms.
+    auto weigh = [&](int nt, float (&w)[4], float (&s)[4]) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[nt][e] = ex2_approx(w[nt][e]);
+        w[e] = ex2_approx(w[e]);
         s[e] = ex2_approx(s[e]);
       }
       l[nt] = f2_add(l[nt], f2_add(f2_pack(s[0], s[1]), f2_pack(s[2], s[3])));
-      p[nt][0] = movmatrix_trans(pack_f16x2(w[nt][0], w[nt][1]));
-      p[nt][1] = movmatrix_trans(pack_f16x2(w[nt][2], w[nt][3]));
+      p[nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+      p[nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+    };
+    float w[NT][4];
+    float top = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const Decode8Heads h = heads(nt);
+      scores(nt, h.f, f2_add(v00, h.nm), f2_add(v11, h.nm), w[nt]);
+      top = max3(top, max3(w[nt][0], w[nt][1], w[nt][2]), w[nt][3]);
+    }
+    if (!__any_sync(0xffffffffu, top > 14.f || fminf(v0, v1) < of_run.v_low)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Decode8Heads h = heads(nt);
+        float s[4];
+        scores(nt, h.f, h.nn, h.nn, s);
+        weigh(nt, w[nt], s);
+      }
+    } else {
+      // A weight more than 2^8 off its bound (or none yet), or a value so much smaller
+      // than the largest that set a bound that a score may be far above n although its
+      // weight is not above m: new bounds, the largest so far.  So a score is 105 above
+      // n at most (8 - ev above m, and m that largest exponent above n), and 2^22 terms
+      // of it still add up.  Once n or m is far from 0 every tile comes here.
+      float far = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Decode8Heads h = heads(nt);
+        float s[4], n[2], d[2], b[2];
+        f2_unpack(f2_mul(x[nt][0], h.f), s[0], s[1]);
+        f2_unpack(f2_mul(x[nt][1], h.f), s[2], s[3]);
+        within(s);
+        f2_unpack(h.nn, n[0], n[1]);
+        f2_unpack(h.d, d[0], d[1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float old = -n[u];
+          n[u] = fmaxf(old, decode8_top(fmaxf(s[u], s[u + 2])));
+          s[u] -= n[u];
+          s[u + 2] -= n[u];
+          b[u] = ex2_approx(old - n[u]);
+          const float before = d[u] + (old - n[u]);  // the old m, seen from the new n
+          w[nt][u] = s[u] + v0;
+          w[nt][u + 2] = s[u + 2] + v1;
+          d[u] = fmaxf(before, decode8_top(fmaxf(w[nt][u], w[nt][u + 2])) - 6.f);
+          w[nt][u] -= d[u];
+          w[nt][u + 2] -= d[u];
+          const float a = ex2_approx(before - d[u]);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            acc[nt][c][u] *= a;
+            acc[nt][c][u + 2] *= a;
+          }
+          far = max3(far, fabsf(n[u]), fabsf(n[u] + d[u]));
+        }
+        l[nt] = f2_mul(l[nt], f2_pack(b[0], b[1]));
+        __syncwarp();  // all lanes have read what is replaced
+        set_heads(nt, {h.f, f2_pack(-n[0] - d[0], -n[1] - d[1]), f2_pack(-n[0], -n[1]), f2_pack(d[0], d[1])}, grp);
+        weigh(nt, w[nt], s);
+      }
+      const float v = decode8_top(fmaxf(v0, v1)) - 97.f;
+      set_factors({of_run.kb, __any_sync(0xffffffffu, far > 512.f) ? INFINITY : fmaxf(of_run.v_low, v)}, lane);
+      __syncwarp();
     }
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
@@ -692,7 +716,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
   const int hl = warp & (p.hb - 1), chunk = warp >> p.hb_log2, parts = kDecode8Parts >> p.hb_log2;
   const int chunks_per_box = p.box / 16;
   const uint32_t rows_at = ((chunk / chunks_per_box * p.hb + hl) * chunks_per_box + chunk % chunks_per_box) * 16 * D;
-  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [3][warp][16 heads]: m, later factors; sums; n
+  float* join = reinterpret_cast<float*>(smem + L::kJoin);  // [3][warp][16 heads]: m - n, later factors; sums; n
   int st = 0;          // place in the ring, and phase of its full barriers
   uint32_t phase = 0;
   bool ok = true;  // false once a wait ran out (recorded): no more waits, and every barrier below is still met
@@ -703,7 +727,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     const int len = p.seq_lens[run.s];
     Decode8Warp<D, NT> w;
     w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_log2, grp, tig,
-            smem + L::kHeads + warp * 256);
+            smem + L::kHeads + warp * (8 * 32 + 16));
     for (int tile = run.from; tile < run.to; ++tile) {
       if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);
@@ -727,12 +751,12 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     // ring's next NT places), one thread a head works out what each of the
     // head's warps counts, and all threads add up and write O, 8 values at a
     // time.
-    float minus_m[NT][2], minus_n[NT][2], sum[NT][2];
+    float minus_n[NT][2], m_n[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const Decode8Heads h = w.heads(nt);
-      f2_unpack(h.nm, minus_m[nt][0], minus_m[nt][1]);
       f2_unpack(h.nn, minus_n[nt][0], minus_n[nt][1]);
+      f2_unpack(h.d, m_n[nt][0], m_n[nt][1]);
       f2_unpack(w.l[nt], sum[nt][0], sum[nt][1]);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -761,7 +785,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int at = warp * 16 + nt * 8 + 2 * tig + u;
-          join[at] = -minus_m[nt][u];
+          join[at] = m_n[nt][u];
           join[kDecode8Warps * 16 + at] = sum[nt][u];
           join[2 * kDecode8Warps * 16 + at] = -minus_n[nt][u];
         }
@@ -779,7 +803,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       const int index = min(static_cast<int>(threadIdx.x), 8 * p.group - 1);
       const int part = index & (parts - 1), row = index >> (3 - p.hb_log2);
       const int g = row / p.group, mine_at = (part * p.hb + g) * 16 + row - g * p.group;
-      const float m = join[mine_at], n = join[2 * kDecode8Warps * 16 + mine_at];
+      const float d = join[mine_at], n = join[2 * kDecode8Warps * 16 + mine_at];
       float mx = n;
 #pragma unroll
       for (int off = 1; off < 8; off <<= 1)
@@ -789,7 +813,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       for (int off = 1; off < 8; off <<= 1)
         if (off < parts) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       __syncwarp();
-      if (on) join[mine_at] = ex2_approx(m - mx - 6.f) / sum;  // O = sum over the warps of acc * 2^(m - mx - 6) / sum
+      if (on) join[mine_at] = ex2_approx(n - mx + d - 6.f) / sum;  // O = sum over the warps of acc * 2^(m - mx - 6) / sum
       const float lse2 = mx + log2f(sum);
       if constexpr (CLUSTER) {
         cluster_wait();  // (these warps here, the others below)

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from attention_flashattention_fwd_04_b200 import api
 
 from .test_cache8_gpu import assert_decoded, cache_case, f64, oracle_append, rows, run_decode, widen
@@ -22,6 +23,17 @@ def stored(c, k, v):
     c["kp"].fill_(0x7F), c["vp"].fill_(0xFF), c["sc"].fill_(255)
     c["kp"], c["vp"], c["sc"] = (torch.from_numpy(np.ascontiguousarray(a)) for a in oracle_append(c))
     return c
+
+
+def one_hot(c, L, d, Hkv, scores, v):
+    """Scores of the caller's choice: q is the first unit vector, the scale 1, and k's first value the score."""
+    k = torch.zeros(L, Hkv, d)
+    k[:, :, 0] = scores[:, None]
+    assert torch.equal(k.to(torch.bfloat16).float(), k)
+    c = stored(c, k, v)
+    q = torch.zeros(1, 4 * Hkv, d)
+    q[..., 0] = 1.0
+    return c, q.to(torch.bfloat16)
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -56,17 +68,6 @@ def test_saturated_keys(wide):
     o, lse = run_decode(widen(c) if wide else c, q, scale)
     assert api.device_status() == 0 and torch.isfinite(o).all() and torch.isfinite(lse).all()
     assert_decoded(c, q, scale, o, lse)
-
-
-def one_hot(c, L, d, Hkv, scores, v):
-    """Scores of the caller's choice: q is the first unit vector, the scale 1, and k's first value the score."""
-    k = torch.zeros(L, Hkv, d)
-    k[:, :, 0] = scores[:, None]
-    assert torch.equal(k.to(torch.bfloat16).float(), k)
-    c = stored(c, k, v)
-    q = torch.zeros(1, 4 * Hkv, d)
-    q[..., 0] = 1.0
-    return c, q.to(torch.bfloat16)
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -121,3 +122,39 @@ def test_the_largest_values_and_none(d, L, wide):
     assert np.allclose(lse, want, atol=2.0 ** -17)
     assert np.all(np.abs(o[0, :4, ::2] / TOP - 1) <= 2.0 ** -8) and np.all(np.abs(o[0, :4, 1::2] / -TOP - 1) <= 2.0 ** -8)
     assert not o[0, 4:].any()
+
+
+def oracle_values(c, L):
+    """The values of the case's first sequence [L, Hkv, d]."""
+    return oracle.paged_gather8(c["kp"].numpy(), c["vp"].numpy(), c["sc"].numpy(), c["table"].numpy(), [L], c["ps"])[0][1]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 13, 2.0 ** 16, 2.0 ** 20, 2.0 ** 24, 2.0 ** 28, 2.0 ** 40, 2.0 ** 60, 2.0 ** 100, 2.0 ** 124])
+def test_scores_of_any_size(size, d, wide):
+    """A token at 1.5 * size, the others at most at 1.25 * size: O is its value row and LSE its score.  Thousands at the same score:
+    O is a mean of their values and LSE log n above it.  Parts of a sequence are joined by their LSEs, whose rounding, 2^-24 of them,
+    is that of the parts' weights (twice, for two LSEs): until it counts, O is the mean with equal weights."""
+    L = 2500
+    c = cache_case(250, [0], [L], 2, d, 16)
+    g = torch.Generator().manual_seed(251)
+    v = torch.randn(L, 2, d, generator=g)
+    scores = torch.tensor([1.25, 1.0, -1.5, 0.0])[torch.randint(0, 4, (L,), generator=g)] * size
+    scores[777] = 1.5 * size
+    alone, q = one_hot(c, L, d, 2, scores, v)
+    o, lse = run_decode(widen(alone) if wide else alone, q, 1.0)
+    page, slot = int(alone["table"][0, 777 // 16]), 777 % 16
+    want = alone["vp"][page, slot].view(torch.float8_e4m3fn).double() * torch.exp2(alone["sc"][page, :, slot, 1].double() - 127)[:, None]
+    # a weight, a sum and their quotient: none is off by more than a few 2^-11, which the rounding to bf16 of a value of 4 bits takes back
+    assert np.array_equal(f64(o)[0], np.repeat(want.numpy(), 4, axis=0))
+    assert np.allclose(f64(lse), 1.5 * size, rtol=2.0 ** -22, atol=0)
+    same, q = one_hot(cache_case(252, [0], [L], 2, d, 16), L, d, 2, torch.full((L,), 1.5 * size), v)
+    o, lse = run_decode(widen(same) if wide else same, q, 1.0)
+    cached = np.repeat(oracle_values(same, L), 4, axis=1)
+    o, mean = f64(o)[0], cached.mean(0)
+    off = 2.0 ** -11 + 2.0 ** -12 + 2 * 2.0 ** -24 * 1.5 * size
+    assert np.all(np.abs(o - mean) <= 2.0 ** -8 * np.abs(mean) + off * np.abs(cached).mean(0)) or off > 0.1
+    slack = 2.0 ** -8 * np.abs(o)
+    assert np.all(o <= cached.max(0) + slack) and np.all(o >= cached.min(0) - slack)
+    assert np.allclose(f64(lse), 1.5 * size + np.log(L), rtol=2.0 ** -22, atol=2.0 ** -17)
