@@ -452,7 +452,8 @@ int paged_attn_decode_fp8(const attn_bf16* q, const uint8_t* k_pool, const uint8
   p.hb = pl.hb;
   for (p.hb_log2 = 0; 1 << p.hb_log2 < pl.hb;) ++p.hb_log2;
   p.ctas = pl.ctas;
-  p.scale_log2 = scale * kLog2e;
+  p.scale_mantissa = static_cast<float>(2.0 * std::frexp(static_cast<double>(scale) * kLog2e, &p.scale_exp));  // whatever scale's exponent
+  --p.scale_exp;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int s0 = 0; s0 < num_seqs; s0 += attn::kDecode8MaxSeqs) {  // one launch for up to 1024 sequences
     p.S = std::min(num_seqs - s0, attn::kDecode8MaxSeqs);

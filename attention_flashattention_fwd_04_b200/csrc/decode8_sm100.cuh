@@ -71,7 +71,8 @@ struct Decode8Params {
   int S, Hq, Hkv, group, page_size, max_pages, num_pages, hb, hb_log2, ctas;
   int box;                     // tokens of one TMA box: 16 * 2^i, a divisor of page_size and of a tile's tokens
   uint32_t page_inverse;       // ceil(2^32 / (page_size / 16)); 0 for page_size = 16
-  float scale_log2;
+  float scale_mantissa;        // scale * log2(e) = scale_mantissa * 2^scale_exp, 1 <= scale_mantissa <= 2
+  int scale_exp;
 };
 
 template <int D, int STAGES>
@@ -293,10 +294,10 @@ struct Decode8Warp {
     else if (lane == 0) *shared_factors = f;
   }
 
-  __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_log2, int grp, int tig, uint8_t* heads_at) {
+  __device__ __forceinline__ void begin(const __nv_bfloat16* qrow, int group, float scale_mantissa, int scale_exp, int grp, int tig,
+                                        uint8_t* heads_at) {
     shared = reinterpret_cast<Decode8Heads*>(heads_at) + tig;
     shared_factors = reinterpret_cast<Decode8Factors*>(heads_at + 8 * 32);
-    const int scale_exp = static_cast<int>(__float_as_uint(scale_log2) >> 23) - 127;
     int shifts[NT], least = 126;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -338,9 +339,9 @@ struct Decode8Warp {
     set_factors({__int_as_float((127 - b) << 23), -INFINITY}, 4 * grp + tig);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int e = b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
+      const int e = scale_exp + b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
       const float factor =  // of head grp; wanted: of heads 2 tig (+ 1)
-          fminf(scale_log2 * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
+          fminf(scale_mantissa * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
       set_heads(nt, {f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4)), none, none, 0}, grp);
     }
     __syncwarp();
@@ -726,8 +727,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
     if (run.from == run.to) continue;
     const int len = p.seq_lens[run.s];
     Decode8Warp<D, NT> w;
-    w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_log2, grp, tig,
-            smem + L::kHeads + warp * (8 * 32 + 16));
+    w.begin(p.q + (static_cast<size_t>(run.s) * p.Hq + (run.hg * p.hb + hl) * p.group) * D, p.group, p.scale_mantissa, p.scale_exp,
+            grp, tig, smem + L::kHeads + warp * (8 * 32 + 16));
     for (int tile = run.from; tile < run.to; ++tile) {
       if (ok) ok = mbar_wait(full_bar(st), phase, kErrCache8Wait);
       ok = __all_sync(0xffffffffu, ok);

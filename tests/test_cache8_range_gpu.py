@@ -56,6 +56,19 @@ def test_keys_and_queries_of_any_size(key, query, d, group, wide):
 
 
 @pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("key,query", [(120, 17), (70, 66), (30, 110)])
+def test_scales_below_the_normal_floats(key, query, wide):
+    """A scale of few bits is what it is, not what is left of its product with log2(e)."""
+    c = cache_case(205, [0] * 2, [200, 33], 2, 64, 16)
+    c = stored(c, torch.ldexp(rows(206, 233, 2, 64).float().clamp(-4, 4), torch.tensor(key)), rows(207, 233, 2, 64).float())
+    q = torch.ldexp(rows(208, 2, 8, 64).float().clamp(-4, 4), torch.tensor(query)).to(torch.bfloat16)
+    scale = float(np.float32(5 * 2.0 ** (-(key + query) - 5)))
+    assert 0 < scale < 2.0 ** -126
+    o, lse = run_decode(widen(c) if wide else c, q, scale)
+    assert_decoded(c, q, scale, o, lse)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 def test_saturated_keys(wide):
     """Rows with an infinity are saturated: a legal cache, and finite scores."""
     c = cache_case(210, [0, 0], [90, 700], 2, 128, 16)
