@@ -30,7 +30,7 @@
 //     and less lose some).  The sum q . kc reaches 2^30 with q so scaled: times 2^ek
 //     it would pass fp32's range long before the score does, so that factor is
 //     2^(ek - b), and 2^b is in the other one, of scale and q's own power.  b is 22, or
-//     what the largest of the KV head's queries leaves of it; so nothing overflows on
+//     less where the largest of the KV head's queries needs it; so nothing overflows on
 //     the way to a score while scale max|q| max|k|, over a KV head's queries and its
 //     rows, is below 2^127.
 //   - V's scale goes into the weights before they are rounded:
@@ -333,15 +333,15 @@ struct Decode8Warp {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) acc[nt][c][0] = acc[nt][c][1] = acc[nt][c][2] = acc[nt][c][3] = 0.f;
     }
-    // scale 2^(b - shift) < 2^127 for all heads, or at least finite (a row of zeros makes it 0 then).
-    const int b = max(min(22, 126 - scale_exp + __reduce_min_sync(0xffffffffu, least)), 0);
+    // scale 2^(b - shift) < 2^127 for all heads.
+    const int b = min(22, 126 - scale_exp + __reduce_min_sync(0xffffffffu, least));
     const uint64_t none = f2_pack(INFINITY, INFINITY);
     set_factors({__int_as_float((127 - b) << 23), -INFINITY}, 4 * grp + tig);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int e = scale_exp + b - shifts[nt], half = e >> 1;  // in two steps: 2^e may be out of range
       const float factor =  // of head grp; wanted: of heads 2 tig (+ 1)
-          fminf(scale_mantissa * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23), 3.4e38f);
+          scale_mantissa * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23);
       set_heads(nt, {f2_pack(__shfl_sync(0xffffffffu, factor, 8 * tig), __shfl_sync(0xffffffffu, factor, 8 * tig + 4)), none, none, 0}, grp);
     }
     __syncwarp();

@@ -56,6 +56,20 @@ def test_keys_and_queries_of_any_size(key, query, d, group, wide):
 
 
 @pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("key,query,scale", [(-85, 70, 2.0 ** 16), (-85, 0, 2.0 ** 86), (-70, 100, 2.0 ** 40), (-85, 120, 2.0 ** 60), (-85, -30, 2.0 ** 120)])
+def test_scores_far_from_zero_under_small_keys(key, query, scale, wide):
+    """Queries times scale near fp32's range and beyond it, where the keys bring the scores back: finite, and LSE the largest score."""
+    L = 300
+    c, q = one_hot(cache_case(209, [0], [L], 2, 64, 16), L, 64, 2, torch.ldexp(torch.arange(L) % 7 - 3.0, torch.tensor(key)),
+                   rows(210, L, 2, 64).float())
+    q = torch.ldexp(q.float(), torch.tensor(query)).to(torch.bfloat16)
+    o, lse = run_decode(widen(c) if wide else c, q, scale)
+    assert_decoded(c, q, scale, o, lse)
+    top = 3.0 * 2.0 ** (key + query) * scale
+    assert torch.isfinite(o).all() and (top < 2.0 ** 20 or np.allclose(f64(lse), top, rtol=2.0 ** -22, atol=0))
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("key,query", [(120, 17), (70, 66), (30, 110)])
 def test_scales_below_the_normal_floats(key, query, wide):
     """A scale of few bits is what it is, not what is left of its product with log2(e)."""
