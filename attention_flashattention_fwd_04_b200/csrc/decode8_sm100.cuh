@@ -58,6 +58,7 @@ constexpr int kDecode8RowsLog2 = 7;
 constexpr int kDecode8Rows = 16 * kDecode8Parts;   // cached rows of a tile
 static_assert(kDecode8Rows == 1 << kDecode8RowsLog2, "a tile is 8 warps of 16 rows");
 constexpr int kDecode8MaxSeqs = 1024;              // sequences of one launch
+constexpr float kDecode8PartScale = 0x1p-12f;      // of partial results: hundreds of the largest values still add up
 
 struct Decode8Params {
   const __nv_bfloat16* q;      // [S, Hq, D]
@@ -814,7 +815,8 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       for (int off = 1; off < 8; off <<= 1)
         if (off < parts) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       __syncwarp();
-      if (on) join[mine_at] = ex2_approx(n - mx + d - 6.f) / sum;  // O = sum over the warps of acc * 2^(m - mx - 6) / sum
+      // O = sum over the warps of acc * 2^(m - mx - 6) / sum
+      if (on) join[mine_at] = ex2_approx(n - mx + d - 6.f) / sum * (!CLUSTER && whole ? 1.f : kDecode8PartScale);
       const float lse2 = mx + log2f(sum);
       if constexpr (CLUSTER) {
         cluster_wait();  // (these warps here, the others below)
@@ -889,17 +891,17 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float w = ex2_approx(l[c] - top) * 0x1p-4f;  // 8 results of the largest values still add up
+        const float w = ex2_approx(l[c] - top);
         sum += w;
         x[0] = fmaf(w, a[c].x, x[0]);
         x[1] = fmaf(w, a[c].y, x[1]);
         x[2] = fmaf(w, a[c].z, x[2]);
         x[3] = fmaf(w, a[c].w, x[3]);
       }
-      const float inv = 1.f / sum;
+      const float inv = 1.f / (kDecode8PartScale * sum);
       *reinterpret_cast<uint2*>(p.o + (head + row) * D + 4 * (slot * p.ctas + rank)) =
           make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-      if (slot == 0 && rank == 0) p.lse[head + row] = (top + log2f(sum * 0x1p4f)) * 0.69314718055994530942f;
+      if (slot == 0 && rank == 0) p.lse[head + row] = (top + log2f(sum)) * 0.69314718055994530942f;
     }
   }
 }
@@ -1011,7 +1013,7 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
       for (int e = 0; e < kPer; ++e) out[e] *= a;
 #pragma unroll
       for (int u = 0; u < kFlight; ++u) {
-        const float w = ex2_approx(l[u] - mx - 12.f);  // 2^-12: hundreds of rows of the largest values still add up
+        const float w = ex2_approx(l[u] - mx);
         sum += w;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) out[e] = fmaf(w, x[u][e], out[e]);
@@ -1042,11 +1044,11 @@ __global__ void __launch_bounds__(32 * kMerge8Warps) decode8_merge_kernel(const 
     }
     mx = top;
   }
-  const float inv = 1.f / sum;
+  const float inv = 1.f / (kDecode8PartScale * sum);
 #pragma unroll
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(p.o + head * D + lane * kPer + e) = pack_bf16x2(out[e] * inv, out[e + 1] * inv);
-  if (lane == 0) p.lse[head] = (mx + log2f(sum * 0x1p12f)) * 0.69314718055994530942f;
+  if (lane == 0) p.lse[head] = (mx + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace attn

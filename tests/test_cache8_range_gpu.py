@@ -116,7 +116,7 @@ def test_many_small_weights_under_any_value_scale(exponent, d, ps, wide):
 
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("first,last", [(119, -100), (-100, 119), (119, 0), (0, -100), (-100, 0)])
-@pytest.mark.parametrize("rise", [0.0, 60.0, -60.0, 240.0])
+@pytest.mark.parametrize("rise", [0.0, 60.0, -60.0, -80.0, 240.0])
 def test_value_scales_and_scores_that_change_along_the_sequence(first, last, rise, wide):
     """Values of one scale under scores of one height, then of another under another."""
     L, half, d = 1500, 700, 64
