@@ -218,15 +218,15 @@ bool decode8_plan(int num_seqs, int Hq, int Hkv, int d, int max_pages, int page_
   // Clusters, where one a sequence and KV head fills no more than the SMs hold
   // and a CTA has few tiles: no partial results and no second launch, but no even
   // shares either.  Up to 8 tiles where they fill half the SMs or more (16
-  // sequences of 2000 tokens, 8 KV heads: 17.6 us against 21.9; one of 2000 among
-  // 15 of 100: 12.7 against 12.8; with up to 16, one of 4000 among 15: 20.1 against
-  // 13.3), else 4 (one of 4000 tokens, 8 KV heads: 8.6 against 10.9; of 8000, 2 KV
-  // heads, d = 64, 8 tiles: 12.4 against 9.4).
+  // sequences of 2000 tokens, 8 KV heads: 17.7 us against 22.0; one of 2000 among
+  // 15 of 100: 12.8 against 12.8; with up to 16, one of 4000 among 15: 20.2 against
+  // 13.5), else 4 (one of 4000 tokens, 8 KV heads: 8.6 against 11.0; of 8000, 2 KV
+  // heads, d = 64, 8 tiles: 12.5 against 9.6).
   // An SM group whose SMs do not divide by the cluster's leaves some out: 33
   // clusters of 8 are there at once with two CTAs an SM, 15 with one, 71 and 33 of
   // 4.  The rooms stay below that, as the last one to wait doubles the time (16
-  // sequences of 1000 tokens, 16 query heads of one KV head: 14.9 us in clusters
-  // of 8, 8.5 of 4).
+  // sequences of 1000 tokens, 16 query heads of one KV head: 15.4 us in clusters
+  // of 8, 8.8 of 4).
   const long long heads = static_cast<long long>(num_seqs) * Hkv, head_tiles = (max_tokens + attn::kDecode8Rows - 1) / attn::kDecode8Rows;
   const int per_sm = group <= 8 || d == 64 ? 2 : 1;
   auto room = [&](int ctas) { return per_sm * (ctas == 8 ? 112 : 128); };
@@ -289,10 +289,10 @@ int launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const attn::Dec
   if (e != cudaSuccess) return fail_cuda(e);
   // Warps for a head's partial rows, about CTAs / (sequences x groups of heads) of
   // them: a warp takes 4 or 8 at a time, so one warp makes many trips to memory
-  // where there are many (16 sequences of 1000 tokens, 18 rows: 20.1 us with 1,
-  // 16.9 with 8), and many warps are idle blocks where there are few (the same
-  // with 16: 24.7; 64 of 1000, 5 rows: 40.9 with 8, 33.0 with 2; 4 of 1000, 74
-  // rows: 10.2 with 16, 15.7 with 2).
+  // where there are many (16 sequences of 1000 tokens, 18 rows: 20.3 us with 1,
+  // 17.1 with 8), and many warps are idle blocks where there are few (the same
+  // with 16: 24.9; 64 of 1000, 5 rows: 41.0 with 8, 33.1 with 2; 4 of 1000, 74
+  // rows: 10.4 with 16, 15.7 with 2).
   const long long heads = static_cast<long long>(p.S) * (p.Hkv / p.hb);
   const int per = p.ctas > 48 * heads ? 16 : p.ctas > 12 * heads ? 8 : p.ctas > 2 * heads ? 2 : 1;
   auto* merge = per == 16  ? attn::decode8_merge_kernel<D, 16>

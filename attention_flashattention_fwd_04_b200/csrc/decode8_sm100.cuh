@@ -9,13 +9,13 @@
 // so that all SMs finish together.  Where a share is many tiles, the begin of a
 // sequence counts as up to 3 more: that is what it costs to write one result and
 // set up the next (16 sequences of 4000 to 8200 tokens, 16 query heads a KV head of
-// d = 128: 34.4 us without, 31.8 with it).  A run that covers the whole of a sequence's
+// d = 128: 34.6 us without, 32.4 with it).  A run that covers the whole of a sequence's
 // tiles writes its output; others write partial results, at most two a CTA,
 // which decode8_merge_kernel joins.
 //
 // Few and short sequences go without the merge: a cluster of up to 8 CTAs has one
 // sequence and KV head, and joins its results through its CTAs' shared memory
-// (one sequence of 1000 tokens: 6.3 us against 7.9, and one launch less).
+// (one sequence of 1000 tokens: 6.4 us against 8.1, and one launch less).
 //
 // A producer warp brings tiles into a ring (codes by TMA, scales by cp.async);
 // each of the 8 consumer warps works on 16 of the tile's rows, 16 tokens of one
@@ -273,7 +273,7 @@ struct Decode8Warp {
   uint32_t q[NT][D / 16][2];
   // Where registers are short the heads' values are in shared memory, a place for
   // each pair: loads cost less than what is spilled otherwise (64 sequences, d = 128:
-  // 99.3 us against 100.7; 3 x 131072 tokens, two head tiles, d = 64: 29.0 against 33.8).
+  // 99.5 us against 102.1; 3 x 131072 tokens, two head tiles, d = 64: 29.5 against 34.0).
   static constexpr bool kShared = NT == 2 || D == 128;
   Decode8Heads* shared;
   Decode8Heads own[kShared ? 1 : NT];
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(Decode8Layout<D, STAGES>::kThreads, PER_SM)
       const uint32_t k = base + st * L::kStage + rows_at, sc = base + L::kScales + (st * kDecode8Parts + warp) * 32;
       const int valid = len - tile * tokens - chunk * 16;
       // Two head tiles have a path without the selects; one loses by the code's size
-      // (one sequence of 1000 tokens: 6.5 against 6.3 us; 64 sequences: 99.8 against 99.3).
+      // (64 sequences: 100.6 us against 99.5; 16 of 4000 tokens: 33.9 against 32.4).
       if (NT == 2 && valid >= 16)
         w.template tile<false>(k, k + L::kPool, sc, 16, lane);
       else if (valid > 0)

@@ -463,11 +463,12 @@ int paged_kv_gather_fp8(const uint8_t* k_pool, const uint8_t* v_pool, const uint
  * and LSE = -inf and is no error; a negative or too long one is reported
  * (bit 14) with the same outputs; a table entry outside the pool is reported and
  * leaves its sequence's outputs unspecified.  Scores, softmax statistics and sums
- * are fp32; queries and keys may be of any size as long as scale * max|q| * max|k|,
- * over the queries of a KV head and its rows, is below 2^127.  A softmax weight,
- * times its value's scale, is rounded to fp16 against the largest of them: to 11
- * bits, or to 2^-31 of the largest where that is more.  Slots past seq_len, their
- * scales too, may hold anything.
+ * are fp32; queries, keys and scale may be of any size as long as
+ * scale * max|q| * max|k|, over the queries of a KV head and its rows, is below
+ * 2^127.  A softmax weight, times its value's scale, is rounded to fp16 against the
+ * largest of them: to 11 bits, or to 2^-31 of the largest where that is more; a
+ * weight below 2^-126 may count as 0.  Slots past seq_len, their scales too, may hold
+ * anything.
  * The workspace's contents do not matter; calls that can overlap need one each,
  * captured graphs that can be replayed at the same time among them.
  * paged_attn_decode_fp8_workspace_bytes: its size; 0 for invalid sizes, and for
